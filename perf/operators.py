@@ -211,13 +211,13 @@ def _e2m1(v):
 
 
 def _quad(e):
-    """Scale exponents [T, K/32] as the product reads them: [K/128, T + 256, 4, 4], entry (kb, r, c, j) the
+    """Scale exponents [T, K/32] as the product reads them: [K/128, T, 4, 4], entry (kb, r, c, j) the
     scale of block 4 kb + j of row r + 32 c, zero bytes past the last row."""
     T, nb = e.shape
-    rows = torch.zeros(T + 352, nb, dtype=torch.uint8, device=e.device)
+    rows = torch.zeros(T + 96, nb, dtype=torch.uint8, device=e.device)
     rows[:T] = (e + 127).to(torch.uint8)
-    rows = rows.view(T + 352, nb // 4, 4).transpose(0, 1)
-    return torch.stack([rows[:, 32 * c: 32 * c + T + 256] for c in range(4)], dim=2).reshape(-1)
+    rows = rows.view(T + 96, nb // 4, 4).transpose(0, 1)
+    return torch.stack([rows[:, 32 * c: 32 * c + T] for c in range(4)], dim=2).reshape(-1)
 
 
 def _run_norm(s):
@@ -318,7 +318,7 @@ def exact(case, seed):
         y = h / torch.sqrt((h * h).mean(1, keepdim=True) + 1e-6) * s["w"].double()
         q, e = _mx64(y, 8)
         T, K = y.shape
-        at = torch.arange(T + 256, device=y.device).view(1, -1, 1, 1) + 32 * torch.arange(4, device=y.device).view(1, 1, 4, 1)
+        at = torch.arange(T, device=y.device).view(1, -1, 1, 1) + 32 * torch.arange(4, device=y.device).view(1, 1, 4, 1)
         block = 4 * torch.arange(K // 128, device=y.device).view(-1, 1, 1, 1) + torch.arange(4, device=y.device)
         scales = torch.where(at < T, _two_to(e)[at.clamp(max=T - 1), block], 2.0 ** -127)
         return {"h": h if s["r"] is not None else None, "y": y if s["y"] else None, "codes": q.reshape(T, K),
