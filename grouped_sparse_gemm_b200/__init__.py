@@ -30,13 +30,17 @@ __all__ = [
     "grouped_sparse_gemm", "grouped_sparse_gemm_swiglu", "grouped_sparse_gemm_combine", "combine_workspace",
     "grouped_dense_gemm", "grouped_dense_gemm_native", "unpermute_scale", "OP_COMBINE", "OP_DISPATCH",
     "get_device_status",
+    "PackedMxWeights", "MxActivations", "pack_mxfp4", "pack_mxfp4_codes", "quantize_act_mx", "grouped_mx_gemm",
+    "OP_QUANTIZE_MX", "MXFP4", "MXFP8",
     "save_packed", "load_packed",
     "act_scales_bytes", "workspace_size", "OP_PACK_SPARSE", "OP_PACK_DENSE", "OP_ROUTE",
     "OP_QUANTIZE", "OP_GEMM", "EXPORTED_SYMBOLS",
 ]
 
 OP_PACK_SPARSE, OP_PACK_DENSE, OP_ROUTE, OP_QUANTIZE, OP_GEMM, OP_COMBINE, OP_DISPATCH = 1, 2, 3, 4, 5, 6, 7
+OP_QUANTIZE_MX = 8
 OUT_BF16, OUT_F32 = 0, 1
+MXFP4, MXFP8 = 4, 8
 ACT_SCALE_PAD_ROWS = 256
 
 EXPORTED_SYMBOLS = [
@@ -48,6 +52,8 @@ EXPORTED_SYMBOLS = [
     "gsg_moe_route_permute_noalloc", "gsg_grouped_sparse_gemm_swiglu", "gsg_grouped_sparse_gemm_combine",
     "gsg_moe_dispatch_nvfp4", "gsg_test_set_gemm_stall_ns", "gsg_grouped_dense_gemm_native",
     "gsg_test_set_gemm_table_cap",
+    "gsg_mx_packed_bytes", "gsg_mx_act_codes_bytes", "gsg_mx_act_scales_bytes", "gsg_pack_mxfp4",
+    "gsg_pack_mxfp4_codes", "gsg_quantize_act_mx", "gsg_grouped_mx_gemm",
 ]
 
 _STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported shape", -3: "CUDA error",
@@ -102,6 +108,13 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         "gsg_grouped_sparse_gemm_combine": (i, [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, vp, vp, vp, sz, vp, vp]),
         "gsg_test_set_gemm_stall_ns": (None, [ctypes.c_ulonglong]),
         "gsg_test_set_gemm_table_cap": (None, [ctypes.c_int]),
+        "gsg_mx_packed_bytes": (sz, [i, i, i]),
+        "gsg_mx_act_codes_bytes": (sz, [i, i, i]),
+        "gsg_mx_act_scales_bytes": (sz, [i, i]),
+        "gsg_pack_mxfp4": (i, [vp, i, i, i, i, vp, vp]),
+        "gsg_pack_mxfp4_codes": (i, [vp, vp, i, i, i, vp, vp]),
+        "gsg_quantize_act_mx": (i, [vp, i, i, i, vp, i, vp, vp, vp, sz, vp]),
+        "gsg_grouped_mx_gemm": (i, [vp, vp, i, vp, vp, i, i, i, i, i, vp, i, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -208,6 +221,34 @@ class QuantizedActivations:
     R: int
     K: int
     sf_block: int
+
+
+MX_CHUNK_BYTES = 17408         # one (expert, n-tile, 256-wide K chunk) block: codes | scales
+
+
+@dataclass
+class PackedMxWeights:
+    packed: torch.Tensor   # uint8 [E*N*K*17/32], MXFP4 chunk blocks (see include/gsg.h)
+    E: int
+    N: int
+    K: int
+
+    def nbytes(self) -> int:
+        return self.packed.numel()
+
+    def expert(self, e: int) -> "PackedMxWeights":
+        """View of expert e alone (E = 1)."""
+        n = self.packed.numel() // self.E
+        return PackedMxWeights(self.packed[e * n:(e + 1) * n], 1, self.N, self.K)
+
+
+@dataclass
+class MxActivations:
+    codes: torch.Tensor     # uint8 [R, K/2] (MXFP4) or [R, K] (MXFP8, E4M3)
+    scales: torch.Tensor    # uint8 [K/128 * R * 16], UE8M0, quad layout without padding rows
+    R: int
+    K: int
+    fmt: int                # MXFP4 (4) or MXFP8 (8)
 
 
 # ------------------------------------------------------------------ storage
@@ -468,6 +509,126 @@ def grouped_dense_gemm_native(act: QuantizedActivations, w: PackedDenseWeights, 
     _check("gsg_grouped_dense_gemm_native", lib().gsg_grouped_dense_gemm_native(
         _ptr(act.codes), _ptr(act.scales), _ptr(act.x_scale), _ptr(w.packed), _ptr(w.w_scale),
         _ptr(offsets), w.E, w.N, w.K, act.R, max_rows_per_expert, _ptr(out), ydt, _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------------ microscaled experts
+def _args(stream, *ts: Optional[torch.Tensor]) -> int:
+    """The checks of the tensors of one call (CUDA, contiguous, on the current device, where the kernels
+    run) and the stream to launch on."""
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("grouped_sparse_gemm_b200 works on CUDA tensors only (no CPU fallback)")
+        if t.get_device() != dev:
+            raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is cuda:{dev}")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _out(t: Optional[torch.Tensor], shape, dtype, device, what: str) -> torch.Tensor:
+    """A new output, or the caller's after a check of its shape and type."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} {dtype}")
+    return t
+
+
+def _ptr_of(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _mx_activations(out: Optional[MxActivations], R: int, K: int, fmt: int, device) -> MxActivations:
+    if fmt not in (MXFP4, MXFP8):
+        raise ValueError(f"fmt {fmt!r}: MXFP4 (4) or MXFP8 (8)")
+    codes, scales = (None, None) if out is None else (out.codes, out.scales)
+    codes = _out(codes, (R, K * fmt // 8), torch.uint8, device, "codes")
+    scales = _out(scales, (K // 128 * R * 16,), torch.uint8, device, "scales")
+    if out is None:
+        return MxActivations(codes, scales, R, K, fmt)
+    if (out.R, out.K, out.fmt) != (R, K, fmt):
+        raise ValueError(f"out: R={out.R} K={out.K} fmt={out.fmt}, expected R={R} K={K} fmt={fmt}")
+    return out
+
+
+def _mx_weights(out: Optional[PackedMxWeights], E: int, N: int, K: int, device) -> PackedMxWeights:
+    n = int(lib().gsg_mx_packed_bytes(E, N, K))
+    if out is not None and (out.E, out.N, out.K) != (E, N, K):
+        raise ValueError(f"out: E={out.E} N={out.N} K={out.K}, expected E={E} N={N} K={K}")
+    packed = _out(None if out is None else out.packed, (n,), torch.uint8, device, "packed")
+    return out if out is not None else PackedMxWeights(packed, E, N, K)
+
+
+def pack_mxfp4(W: torch.Tensor, out: Optional[PackedMxWeights] = None, stream=None) -> PackedMxWeights:
+    """W fp32 or bf16 [E, N, K] -> MXFP4 packed weights (gsg_pack_mxfp4)."""
+    if W.dim() != 3 or W.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"W: fp32 or bf16 [E, N, K] wanted, got {W.dtype} {tuple(W.shape)}")
+    E, N, K = W.shape
+    s = _args(stream, W, None if out is None else out.packed)
+    out = _mx_weights(out, E, N, K, W.device)
+    _check("gsg_pack_mxfp4", lib().gsg_pack_mxfp4(
+        W.data_ptr(), OUT_F32 if W.dtype == torch.float32 else OUT_BF16, E, N, K, out.packed.data_ptr(), s))
+    return out
+
+
+def pack_mxfp4_codes(codes: torch.Tensor, scales: torch.Tensor, out: Optional[PackedMxWeights] = None,
+                     stream=None) -> PackedMxWeights:
+    """MXFP4 weights as checkpoints store them (codes uint8 [E, N, K/2], low nibble = even k; scale bytes
+    uint8 [E, N, K/32]) -> packed weights, values unchanged (gsg_pack_mxfp4_codes)."""
+    if codes.dim() != 3 or codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise ValueError("codes uint8 [E, N, K/2] and scales uint8 [E, N, K/32] wanted")
+    E, N, K = codes.shape[0], codes.shape[1], codes.shape[2] * 2
+    if tuple(scales.shape) != (E, N, K // 32):
+        raise ValueError(f"scales: {tuple(scales.shape)}, expected {(E, N, K // 32)}")
+    s = _args(stream, codes, scales, None if out is None else out.packed)
+    out = _mx_weights(out, E, N, K, codes.device)
+    _check("gsg_pack_mxfp4_codes", lib().gsg_pack_mxfp4_codes(
+        codes.data_ptr(), scales.data_ptr(), E, N, K, out.packed.data_ptr(), s))
+    return out
+
+
+def quantize_act_mx(X: torch.Tensor, fmt: int = MXFP8, inv_perm: Optional[torch.Tensor] = None, top_k: int = 1,
+                    out: Optional[MxActivations] = None, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> MxActivations:
+    """X bf16 [T, K] -> MXFP4 or MXFP8 codes and scales in routed row order (gsg_quantize_act_mx)."""
+    if X.dim() != 2 or X.dtype != torch.bfloat16:
+        raise ValueError(f"X: bf16 [T, K] wanted, got {X.dtype} {tuple(X.shape)}")
+    T, K = X.shape
+    if inv_perm is not None and (inv_perm.dtype != torch.int32 or inv_perm.numel() < T * top_k):
+        raise ValueError(f"inv_perm: int32 of {T * top_k} entries wanted")
+    s = _args(stream, X, inv_perm, workspace, None if out is None else out.codes, None if out is None else out.scales)
+    out = _mx_activations(out, T * top_k, K, fmt, X.device)
+    L = lib()
+    if workspace is None and T * top_k * K >= 1 << 27:   # (below that the call needs none)
+        workspace = _workspace(L.gsg_workspace_size(OP_QUANTIZE_MX, 0, 0, K, T, top_k), X.device)
+    _check("gsg_quantize_act_mx", L.gsg_quantize_act_mx(
+        X.data_ptr(), T, K, fmt, _ptr_of(inv_perm), top_k, out.codes.data_ptr(), out.scales.data_ptr(),
+        _ptr_of(workspace), 0 if workspace is None else workspace.numel(), s))
+    return out
+
+
+def grouped_mx_gemm(act: MxActivations, w: PackedMxWeights, offsets: torch.Tensor, max_rows_per_expert: int = -1,
+                    out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                    stream=None) -> torch.Tensor:
+    """Y [R, N] = per-expert X_e . W_e^T on MXFP4 weights, MXFP4 or MXFP8 activations
+    (gsg_grouped_mx_gemm).  One expert with offsets [0, R] is a plain linear layer."""
+    if act.K != w.K:
+        raise ValueError(f"activations have K = {act.K}, weights K = {w.K}")
+    if offsets.dtype != torch.int32 or offsets.numel() != w.E + 1:
+        raise ValueError(f"offsets: int32 of {w.E + 1} entries wanted")
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out: bf16 or fp32, got {out_dtype}")
+    s = _args(stream, act.codes, act.scales, w.packed, offsets, out)
+    out = _out(out, (act.R, w.N), out_dtype, act.codes.device, "out")
+    _check("gsg_grouped_mx_gemm", lib().gsg_grouped_mx_gemm(
+        act.codes.data_ptr(), act.scales.data_ptr(), act.fmt, w.packed.data_ptr(), offsets.data_ptr(), w.E, w.N, w.K,
+        act.R, max_rows_per_expert, out.data_ptr(), OUT_F32 if out_dtype == torch.float32 else OUT_BF16, s))
     return out
 
 

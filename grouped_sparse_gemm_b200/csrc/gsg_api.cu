@@ -46,6 +46,7 @@ gsg_status_t device_state(DeviceState** out) {
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned128(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 127u) == 0; }
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 inline gsg_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? GSG_OK : GSG_ERR_CUDA; }
 
@@ -103,6 +104,9 @@ size_t gsg_workspace_size(int op, int E, int N, int K, int T, int k) {
       return (gsg::route_workspace_bytes(T * k, E) + 255) / 256 * 256 +
              ((size_t)gsg::dispatch_amax_blocks((long long)T * K) * sizeof(float) + 255) / 256 * 256 +
              gsg::quant_raw_bytes((long long)T * k, K);
+    case GSG_OP_QUANTIZE_MX:   // (large R*K) the raw scale words
+      if (T < 0 || K < 1 || k < 1) return 0;
+      return gsg::quant_raw_bytes((long long)T * k, K);
     case GSG_OP_COMBINE:   // slots bf16 [T*k][N], then counters int32 [T][N/32]
       if (T < 0 || k < 1 || N < 32) return 0;
       return combine_slot_bytes(T, k, N) + (size_t)T * (N / 32) * sizeof(int);
@@ -217,6 +221,80 @@ gsg_status_t gsg_moe_dispatch_nvfp4(const int32_t* topk_ids, const uint16_t* X, 
   return from_cuda(e);
 }
 
+size_t gsg_mx_packed_bytes(int E, int N, int K) {
+  return (size_t)E * (N / gsg::kTileN) * (K / gsg::kChunkK) * gsg::kMxChunkBytes;
+}
+size_t gsg_mx_act_codes_bytes(int R, int K, int fmt) { return (size_t)R * K * fmt / 8; }
+size_t gsg_mx_act_scales_bytes(int R, int K) { return (size_t)(K / 128) * (size_t)R * 16; }
+
+// The weight shapes of the microscaled calls: the packed rows are addressed by a 32-bit coordinate.
+static bool mx_shape_ok(int E, int N, int K) {
+  return weight_shape_ok(E, N, K) && gsg::gemm_supported(E) &&
+         (long long)E * (N / gsg::kTileN) * (K / gsg::kChunkK) * gsg::kMxChunkRows < (1ll << 31);
+}
+
+gsg_status_t gsg_pack_mxfp4(const void* W, int w_dtype, int E, int N, int K, uint8_t* w_packed, void* stream) {
+  if (!W || !w_packed || (w_dtype != GSG_OUT_BF16 && w_dtype != GSG_OUT_F32)) return GSG_ERR_INVALID_ARG;
+  if (!mx_shape_ok(E, N, K)) return GSG_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(W) || !aligned128(w_packed)) return GSG_ERR_INVALID_ARG;
+  DeviceState* d = nullptr;
+  gsg_status_t st = device_state(&d);
+  if (st != GSG_OK) return st;
+  return from_cuda(gsg::launch_pack_mxfp4(W, w_dtype == GSG_OUT_F32, E, N, K, w_packed, d->status, as_stream(stream)));
+}
+
+gsg_status_t gsg_pack_mxfp4_codes(const uint8_t* codes, const uint8_t* scales, int E, int N, int K, uint8_t* w_packed,
+                                  void* stream) {
+  if (!codes || !scales || !w_packed) return GSG_ERR_INVALID_ARG;
+  if (!mx_shape_ok(E, N, K)) return GSG_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(codes) || !aligned128(w_packed)) return GSG_ERR_INVALID_ARG;
+  DeviceState* d = nullptr;
+  gsg_status_t st = device_state(&d);
+  if (st != GSG_OK) return st;
+  return from_cuda(gsg::launch_pack_mxfp4_codes(codes, scales, E, N, K, w_packed, d->status, as_stream(stream)));
+}
+
+gsg_status_t gsg_quantize_act_mx(const uint16_t* X, int T, int K, int fmt, const int32_t* inv_perm, int k,
+                                 uint8_t* codes, uint8_t* scales, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  if (T < 0 || k < 1 || (fmt != GSG_MXFP4 && fmt != GSG_MXFP8)) return GSG_ERR_INVALID_ARG;
+  if (K < 256 || K % 256 != 0) return GSG_ERR_UNSUPPORTED_SHAPE;
+  if ((long long)T * k > (1ll << 30)) return GSG_ERR_UNSUPPORTED_SHAPE;
+  if ((long long)T * (K / 16) >= (1ll << 31)) return GSG_ERR_UNSUPPORTED_SHAPE;  // 32-bit unit index
+  if (inv_perm == nullptr && k != 1) return GSG_ERR_INVALID_ARG;
+  if (T == 0) return GSG_OK;
+  if (!X || !codes || !scales) return GSG_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(codes) || !aligned16(scales)) return GSG_ERR_INVALID_ARG;
+  const size_t need = gsg_workspace_size(GSG_OP_QUANTIZE_MX, 0, 0, K, T, k);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))) return GSG_ERR_WORKSPACE;
+  DeviceState* d = nullptr;
+  gsg_status_t st = device_state(&d);
+  if (st != GSG_OK) return st;
+  return from_cuda(gsg::launch_quant_mx(X, T, K, fmt, inv_perm, k, codes, scales,
+                                        need > 0 ? static_cast<uint32_t*>(workspace) : nullptr, d->status, d->num_sms,
+                                        as_stream(stream)));
+}
+
+gsg_status_t gsg_grouped_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int act_fmt, const uint8_t* w_packed,
+                                 const int32_t* expert_offsets, int E, int N, int K, int R, int max_rows_per_expert,
+                                 void* Y, int y_dtype, void* stream) {
+  if (R < 0 || (act_fmt != GSG_MXFP4 && act_fmt != GSG_MXFP8) || (y_dtype != GSG_OUT_BF16 && y_dtype != GSG_OUT_F32))
+    return GSG_ERR_INVALID_ARG;
+  if (!mx_shape_ok(E, N, K)) return GSG_ERR_UNSUPPORTED_SHAPE;
+  if ((long long)R > (1ll << 30)) return GSG_ERR_UNSUPPORTED_SHAPE;
+  if (!expert_offsets || !w_packed) return GSG_ERR_INVALID_ARG;
+  if (R == 0) return GSG_OK;
+  if (!a_codes || !a_scales || !Y) return GSG_ERR_INVALID_ARG;
+  if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned128(w_packed) || !aligned16(Y)) return GSG_ERR_INVALID_ARG;
+  DeviceState* d = nullptr;
+  gsg_status_t st = device_state(&d);
+  if (st != GSG_OK) return st;
+  const int rc = gsg::launch_gemm(act_fmt == GSG_MXFP8 ? gsg::kGemmMx8 : gsg::kGemmMx4, a_codes, a_scales, nullptr,
+                                  w_packed, nullptr, expert_offsets, E, N, K, R, max_rows_per_expert, Y,
+                                  y_dtype == GSG_OUT_F32 ? 1 : 0, d->status, d->num_sms, as_stream(stream));
+  return rc == 0 ? GSG_OK : GSG_ERR_CUDA;
+}
+
 static gsg_status_t gemm_common(bool sparse, const uint8_t* a_codes, const uint8_t* a_scales, const float* x_scale,
                                 const uint8_t* w_packed, const float* w_scale, const int32_t* off, int E, int N,
                                 int K, int R, int max_rows, void* Y, int y_dtype, void* stream,
@@ -231,7 +309,7 @@ static gsg_status_t gemm_common(bool sparse, const uint8_t* a_codes, const uint8
   DeviceState* d = nullptr;
   gsg_status_t st = device_state(&d);
   if (st != GSG_OK) return st;
-  const int rc = gsg::launch_gemm(sparse, a_codes, a_scales, x_scale, w_packed, w_scale, off, E, N, K, R, max_rows,
+  const int rc = gsg::launch_gemm(sparse ? gsg::kGemmSparse : gsg::kGemmDense, a_codes, a_scales, x_scale, w_packed, w_scale, off, E, N, K, R, max_rows,
                                   Y, y_dtype == GSG_OUT_F32 ? 1 : 0, d->status, d->num_sms, as_stream(stream),
                                   nullptr, nullptr, nullptr, native);
   return rc == 0 ? GSG_OK : GSG_ERR_CUDA;
@@ -283,7 +361,7 @@ gsg_status_t gsg_grouped_sparse_gemm_swiglu(const uint8_t* a_codes, const uint8_
   }
   if (!a_codes || !a_scales || !h_codes) return GSG_ERR_INVALID_ARG;
   if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(h_codes)) return GSG_ERR_INVALID_ARG;
-  const int rc = gsg::launch_gemm(true, a_codes, a_scales, x_tensor_scale, w_packed, w_tensor_scale, expert_offsets,
+  const int rc = gsg::launch_gemm(gsg::kGemmSparse, a_codes, a_scales, x_tensor_scale, w_packed, w_tensor_scale, expert_offsets,
                                   E, N2, K, R, max_rows_per_expert, h_codes, 0, d->status, d->num_sms,
                                   as_stream(stream), h_scales, h_tensor_scale);
   return rc == 0 ? GSG_OK : GSG_ERR_CUDA;
@@ -318,7 +396,7 @@ gsg_status_t gsg_grouped_sparse_gemm_combine(const uint8_t* a_codes, const uint8
   ca.counters = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + combine_slot_bytes(T, k, N));
   ca.out = out;
   ca.k = k;
-  const int rc = gsg::launch_gemm(true, a_codes, a_scales, x_tensor_scale, w_packed, w_tensor_scale, expert_offsets,
+  const int rc = gsg::launch_gemm(gsg::kGemmSparse, a_codes, a_scales, x_tensor_scale, w_packed, w_tensor_scale, expert_offsets,
                                   E, N, K, R, max_rows_per_expert, workspace, 0, d->status, d->num_sms,
                                   as_stream(stream), nullptr, nullptr, &ca);
   return rc == 0 ? GSG_OK : GSG_ERR_CUDA;

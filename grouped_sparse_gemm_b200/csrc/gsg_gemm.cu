@@ -56,6 +56,15 @@ constexpr uint32_t kColAcc = kNSets * kSetCols;       // first accumulator (192)
 constexpr int kOutStageBytes = 16 * 32 * 4;           // epilogue transpose buffer per warp
 constexpr int kGluStageBytes = 32 * 36 * 4;           // SwiGLU epilogue: 32 tokens x 32 features (+4 pad)
 
+// Operand formats of an instantiation (weights x activations).
+//  kFmtDense, kFmtSparse: NVFP4 both, UE4M3 block scales and fp32 tensor scales (kind::mxf4nvf4).
+//  kFmtMx4: microscaled 4-bit weights and activations, one UE8M0 scale per 32 values and no tensor
+//    scale (kind::mxf4, K = 64 per MMA).
+//  kFmtMx8: the same weights, E4M3 activations with UE8M0 scales (kind::mxf8f6f4, K = 32 per MMA).
+//    That MMA reads 4-bit operands from 16-byte groups of 16 values (8 bytes of codes, 8 of padding);
+//    the TMA writes that form into shared memory from the packed codes, so HBM and L2 carry 4 bits.
+constexpr int kFmtDense = kGemmDense, kFmtSparse = kGemmSparse, kFmtMx4 = kGemmMx4, kFmtMx8 = kGemmMx8;
+
 struct GemmParams {
   const uint8_t* a_scales;
   const float* x_scale;
@@ -278,6 +287,27 @@ __device__ __forceinline__ void tc_mma_dense_pair(uint32_t d, uint64_t adesc, ui
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
       : "memory");
 }
+// Microscaled forms (dense, one UE8M0 scale per 32 values): 4-bit weights against 4-bit (kM8 false)
+// or 8-bit activations, for one CTA or a CTA pair.  idesc names the bytes of the scale words used.
+template <bool kM8, bool kPair>
+__device__ __forceinline__ void tc_mma_mx(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate, uint32_t sfa, uint32_t sfb) {
+#define GSG_MX_MMA(CG, KIND)                                                                                   \
+  asm volatile(                                                                                                \
+      "{\n\t.reg .pred p, P;\n\t"                                                                              \
+      "setp.ne.b32 p, %4, 0;\n\t" GSG_ELECT                                                                    \
+      "@P tcgen05.mma.cta_group::" CG ".kind::" KIND ".block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d), \
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)                                  \
+      : "memory")
+  if constexpr (kM8) {
+    if constexpr (kPair) GSG_MX_MMA("2", "mxf8f6f4");
+    else GSG_MX_MMA("1", "mxf8f6f4");
+  } else {
+    if constexpr (kPair) GSG_MX_MMA("2", "mxf4");
+    else GSG_MX_MMA("1", "mxf4");
+  }
+#undef GSG_MX_MMA
+}
 // 32 accumulator columns of this lane's TMEM row, times `scale`, rounded to bf16 and packed in
 // pairs: h[i] = column 2i (low half) and column 2i + 1 (high half).
 __device__ __forceinline__ void tc_ld_32_bf16(uint32_t taddr, float scale, uint32_t h[16]) {
@@ -326,6 +356,16 @@ __host__ __device__ inline uint32_t make_idesc(bool sparse, int BN, int M = 128)
   return (sparse ? (1u << 2) : 0u) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
+
+// The microscaled descriptors: UE8M0 scales (bit 23), E2M1 x E2M1 (kind::mxf4) or E2M1 weights x
+// E4M3 activations (kind::mxf8f6f4).
+__host__ __device__ inline uint32_t make_idesc_mx(bool act8, int BN, int M) {
+  return (act8 ? (5u << 7) : (1u << 7) | (1u << 10)) | ((uint32_t)(BN >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(M >> 4) << 24);
+}
+// Descriptor bits for the byte of the 32-bit scale words (one byte per 32 values of a 128-wide k-block)
+// that an MMA's first 32 values use, in both operands.
+__host__ __device__ constexpr uint32_t idesc_sf(int sf) { return ((uint32_t)sf << 4) | ((uint32_t)sf << 29); }
 
 struct Ctl {
   int abort;
@@ -441,9 +481,28 @@ __device__ __forceinline__ int tile_at_cost(long long target, const long long* c
 // byte); 128-token tiles keep two-chunk stages, also on CTA pairs (three-chunk stages, three of
 // them in shared memory, measured slower than five two-chunk stages).  Wide pair tiles: two-chunk
 // stages for the sparse weights (three 62 KB stages; six one-chunk stages measured slower), one
-// chunk for the dense control's larger blocks.
-__host__ __device__ constexpr int stage_chunks(bool sparse, int BN, bool glu, int cg, bool wide = false) {
-  return wide ? (sparse ? 2 : 1) : glu ? 2 : sparse ? (BN <= 32 ? 3 : 2) : (BN <= 32 ? 2 : 1);
+// chunk for the dense control's larger blocks.  The microscaled 4-bit formats follow the dense
+// control; with 8-bit activations a chunk already takes twice the shared memory, so one per stage.
+__host__ __device__ constexpr int stage_chunks(int fmt, int BN, bool glu, int cg, bool wide = false) {
+  return fmt == kFmtMx8 ? 1
+         : wide         ? (fmt == kFmtSparse ? 2 : 1)
+         : glu          ? 2
+                        : fmt == kFmtSparse ? (BN <= 32 ? 3 : 2) : (BN <= 32 ? 2 : 1);
+}
+// Format constants: 512-byte scale atoms per 256-wide chunk, shared-memory bytes of a weight chunk
+// block, activation bytes per row and chunk, and weight bits per 32 x 8 (= bytes per 32 weights).
+__host__ __device__ constexpr bool fmt_mx(int fmt) { return fmt == kFmtMx4 || fmt == kFmtMx8; }
+__host__ __device__ constexpr int fmt_sf_chunk(int fmt) { return fmt == kFmtDense ? 4 : 2; }
+__host__ __device__ constexpr int fmt_w_chunk(int fmt) {
+  return fmt == kFmtSparse ? kSparseChunkBytes
+         : fmt == kFmtDense ? kDenseChunkBytes
+         : fmt == kFmtMx4   ? kMxChunkBytes
+                            : kMxChunkBytes + kMxCodeBytes;
+}
+__host__ __device__ constexpr int fmt_act_chunk(int fmt) { return fmt == kFmtMx8 ? 256 : 128; }
+__host__ __device__ constexpr int fmt_w_bytes32(int fmt) { return fmt == kFmtSparse ? 11 : fmt == kFmtDense ? 18 : 17; }
+__host__ __device__ constexpr int fmt_act_row(int fmt, int K) {   // activation codes + scales of a row
+  return K / 256 * (fmt_act_chunk(fmt) + 4 * fmt_sf_chunk(fmt));
 }
 
 // Compile-time stage geometry of one (sparse/dense, token tile, SwiGLU, CTA group) instantiation.
@@ -453,32 +512,47 @@ __host__ __device__ constexpr int stage_chunks(bool sparse, int BN, bool glu, in
 // by a pair of CTAs on two SMs: CTA r holds n-tile 2*np + r and half of the token rows, and the
 // pair's MMAs (M = 256) read both CTAs' shared memory, so each SM stages its own weights but only
 // half of the shared activation tile.
-template <bool kSparse, int kBN, bool kGLU = false, int kCG = 1, bool kWide = false>
+template <int kFmt, int kBN, bool kGLU = false, int kCG = 1, bool kWide = false>
 struct Geo {
   static_assert(kCG == 1 || (kCG == 2 && !kGLU && kBN == 128), "CTA pairs: 128-token tiles, plain epilogue");
   static_assert(!kWide || kCG == 2, "wide tiles run on CTA pairs");
+  static constexpr bool kSparse = kFmt == kFmtSparse;
+  static constexpr bool kMx = fmt_mx(kFmt);
   static constexpr int kNT = (kGLU || kWide) ? 2 : 1;              // weight n-tiles per tile (per CTA)
-  static constexpr int kKbLogical = kSparse ? 128 : 64;            // logical K per MMA
-  static constexpr int kKbPerChunk = kChunkK / kKbLogical;         // 2 sparse, 4 dense
+  static constexpr int kKbLogical = kSparse ? 128 : kFmt == kFmtMx8 ? 32 : 64;   // logical K per MMA
+  static constexpr int kKbPerChunk = kChunkK / kKbLogical;         // MMAs per chunk: 2 sparse, 4, 8 with 8-bit tokens
+  static constexpr int kSfPerChunk = fmt_sf_chunk(kFmt);           // scale atoms per chunk
+  static constexpr int kMmaPerSf = kKbPerChunk / kSfPerChunk;      // MMAs that share an atom (1 for NVFP4)
+  static constexpr int kSfIdStep = 4 / kMmaPerSf;                  // scale bytes each of them uses
   // 256-wide K chunks per stage: short token tiles take longer stages (fewer waits per weight byte)
-  static constexpr int kCPS = stage_chunks(kSparse, kBN, kGLU, kCG, kWide);
-  static constexpr int kKbps = kCPS * kKbPerChunk;                 // k-blocks per stage
-  static constexpr int kCB = kSparse ? kSparseChunkBytes : kDenseChunkBytes;   // packed chunk block
+  static constexpr int kCPS = stage_chunks(kFmt, kBN, kGLU, kCG, kWide);
+  static constexpr int kSfps = kCPS * kSfPerChunk;                 // scale atoms per stage
+  static constexpr int kCB = fmt_w_chunk(kFmt);                    // weight chunk block in shared memory
   static constexpr int kCBMeta = 8192;                             // metadata offset in a chunk block
-  static constexpr int kCBScale = kSparse ? 10240 : 16384;         // scale atoms offset in a chunk block
+  static constexpr int kCBScale = kSparse ? 10240 : kCB - 512 * kSfPerChunk;   // scale atoms offset in a chunk block
   static constexpr int kBRows = kBN / kCG;                         // token rows this CTA stages
-  static constexpr int kBChunk = kBRows * 128;                     // activation codes per chunk
+  static constexpr int kHalves = kFmt == kFmtMx8 ? 2 : 1;          // 128-byte wide token tiles per chunk
+  static constexpr int kBChunk = kBRows * 128 * kHalves;           // activation codes per chunk
   static constexpr int kOffW = kCPS * kBChunk;                     // stage layout: B chunks | W blocks | SFB
   static constexpr int kOffSFB = kOffW + kNT * kCPS * kCB;
-  static constexpr int kStage = (kOffSFB + kKbps * 512 + 1023) / 1024 * 1024;
+  static constexpr int kStage = (kOffSFB + kSfps * 512 + 1023) / 1024 * 1024;
   static constexpr int kMetaCols = kSparse ? 4 * kCPS * kNT : 0;   // TMEM set: meta | SFA | SFB
   static constexpr int kColSFA = kMetaCols;
-  static constexpr int kColSFB = kMetaCols + 4 * kKbps * kNT;
-  static constexpr int kSetUsed = kColSFB + 4 * kKbps;
+  static constexpr int kColSFB = kMetaCols + 4 * kSfps * kNT;
+  static constexpr int kSetUsed = kColSFB + 4 * kSfps;
   static constexpr uint32_t kBStep = kSparse ? 64 : 32;            // B bytes per row per MMA
   static constexpr int kBoxH = kBRows < 32 ? kBRows : 32;          // token rows per TMA box
   static constexpr int kAccStride = kBN < 32 ? 32 : kBN;
   static_assert(kSetUsed <= (int)kSetCols, "TMEM set too small");
+  // Operand A / B shared-memory descriptors' offsets of MMA h of a chunk: the NVFP4 weights are stored
+  // as the MMA's core matrices, 4096 bytes per MMA; the microscaled weights and all tokens are 128-byte
+  // swizzled rows, of which an MMA takes kBStep bytes (8-bit tokens: two row tiles per chunk).
+  __device__ static constexpr uint32_t a_off(int h) {
+    return !kMx ? 4096u * h : kHalves == 2 ? (h / 4) * (uint32_t)kMxCodeBytes + 32u * (h % 4) : 32u * h;
+  }
+  __device__ static constexpr uint32_t b_off(int h) {
+    return kHalves == 2 ? (h / 4) * (uint32_t)(kBRows * 128) + 32u * (h % 4) : kBStep * h;
+  }
 };
 
 // kCG = 2: launched as clusters of two CTAs (a CTA pair on two SMs) that run 256-row weight tiles
@@ -564,15 +638,16 @@ __device__ void combine_tokens(const GemmParams& p, volatile int* abort_flag) {
   }
 }
 
-template <bool kSparse, int kBN, bool kGLU, int kCG, bool kNative = false, bool kWide = false>
+template <int kFmt, int kBN, bool kGLU, int kCG, bool kNative = false, bool kWide = false>
 __global__ void __launch_bounds__(gemm_threads(kWide), 1)
 grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant__ CUtensorMap tmap_b64,
-                    const __grid_constant__ CUtensorMap tmap_sfb,
+                    const __grid_constant__ CUtensorMap tmap_sfb, const __grid_constant__ CUtensorMap tmap_w,
                     const GemmParams p) {
-  using G = Geo<kSparse, kBN, kGLU, kCG, kWide>;
+  using G = Geo<kFmt, kBN, kGLU, kCG, kWide>;
+  constexpr bool kSparse = G::kSparse, kMx = G::kMx;
   constexpr int kThreads = gemm_threads(kWide);
   constexpr bool kPair = kCG == 2;
-  static_assert(!kNative || (!kSparse && kBN == 128 && !kGLU && kCG == 1), "native orientation: dense, 128 tokens");
+  static_assert(!kNative || (kFmt == kFmtDense && kBN == 128 && !kGLU && kCG == 1), "native orientation: dense, 128 tokens");
   extern __shared__ uint8_t smem_raw[];
   // NT: weight n-tiles; tiles run over NT / (kNT * kCG) columns (the gate n-tiles with the SwiGLU
   // epilogue, n-tile pairs for CTA pairs)
@@ -613,6 +688,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_b)) : "memory");
     if (kBN >= 64) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_b64)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_sfb)) : "memory");
+    if (kMx) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_w)) : "memory");
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) { mbar_init(full_bar(s), 2); mbar_init(empty_bar(s), 1); }
@@ -647,7 +723,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
     int v = __ldg(p.off + i);
     if (v < 0 || v > p.R) { bad = true; v = v < 0 ? 0 : p.R; }
     offs[i] = v;
-    if (i < E) wsc[i] = __ldg(p.w_scale + i);
+    if (i < E) wsc[i] = kMx ? 1.0f : __ldg(p.w_scale + i);
   }
   if (kGLU) {
     // h scale entries that refer to rows >= R (no tile writes them): zero, shared by the CTAs
@@ -689,8 +765,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
     if (threadIdx.x == kThreads - 1) pref[E] = before + incl;
   }
   // bytes per tile: weights wc, plus ac per token row (codes, scales, output row segment)
-  const long long wc = (long long)G::kNT * kCG * kTileN * p.K * (kSparse ? 11 : 18) / 32;
-  const long long ac = p.K / 2 + p.K / (kSparse ? 32 : 16) + (long long)G::kNT * kCG * kTileN * (p.y_f32 ? 4 : 2);
+  const long long wc = (long long)G::kNT * kCG * kTileN * p.K * fmt_w_bytes32(kFmt) / 32;
+  const long long ac = fmt_act_row(kFmt, p.K) + (long long)G::kNT * kCG * kTileN * (p.y_f32 ? 4 : 2);
   if (p.sched == kSchedRuns) {   // (only the byte-balanced schedule reads the costs; uniform branch)
     // chunked exclusive scan of cost_e = NTt * (ceil(rows_e / BN) * wc + rows_e * ac)
     const int per = (E + kThreads - 1) / kThreads;
@@ -763,10 +839,12 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
       const TileDesc c = my_tile(j, ttab, p.tcap, pref, offs, E, kBN, p.sched, tb, unit, nunits);
       // this CTA's first weight n-tile: tile c.nt spans n-tiles [c.nt * kCG * kNT, +kCG * kNT) of the
       // expert (SwiGLU: the gate n-tiles only), CTA r of a pair takes every other one from r
-      const uint8_t* wsrc =
-          p.w_packed + ((size_t)c.e * NT + c.nt * kCG * (kWide ? 2 : 1) + rank) * KC * G::kCB;
+      constexpr int kPackedCB = kMx ? kMxChunkBytes : G::kCB;   // chunk block in the packed weights
+      const size_t wblk = ((size_t)c.e * NT + c.nt * kCG * (kWide ? 2 : 1) + rank) * KC;   // its first chunk block
+      const uint8_t* wsrc = p.w_packed + wblk * kPackedCB;
       // its second n-tile: SwiGLU, the matching up n-tile; a wide pair tile, the next pair's
-      const uint8_t* wsrc_up = wsrc + (size_t)(kWide ? kCG : NT / 2) * KC * G::kCB;
+      const size_t wup = (size_t)(kWide ? kCG : NT / 2) * KC;
+      const uint8_t* wsrc_up = wsrc + wup * kPackedCB;
       // this CTA's token rows [r0, r0 + cnt): all of the tile's, or for a CTA pair the half of the
       // MMA's N = valid rounded up to 16 that this CTA supplies (rank 1: the upper half)
       const int nh = kPair ? ((c.valid + 15) & ~15) / 2 : kBN;
@@ -788,20 +866,35 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
           // n-tile t (t = 1: the SwiGLU up n-tile); lane 31 copies the activation scale atoms of the
           // whole tile's tokens from its first row (in both CTAs of a pair: each CTA's MMA share
           // needs the scales of all N token columns)
-          mbar_arrive_expect_tx(fb, (uint32_t)(G::kNT * nch * G::kCB + G::kKbps * 512));
-          const int t = lane / nch, ch = lane - t * nch;
-          bulk_g2s_lane(lane < G::kNT * nch, st + G::kOffW + (t * G::kCPS + ch) * G::kCB,
-                        (t == 0 ? wsrc : wsrc_up) + (size_t)(kc + ch) * G::kCB, G::kCB, fb);
-          tma_load_3d_lane(lane == 31, st + G::kOffSFB, &tmap_sfb, 0, c.r0, kc * G::kKbPerChunk, fb);
+          // (the 4-bit codes that a copy widens for 8-bit activations still count as they lie in HBM)
+          mbar_arrive_expect_tx(fb, (uint32_t)(G::kNT * nch * kPackedCB + G::kSfps * 512));
+          if constexpr (kMx) {
+            // per chunk block: the 128 rows of codes (256 values; for 8-bit activations two copies of 128
+            // values, which the TMA widens to 128 bytes each), then the block's two scale atoms
+            const int u = lane / G::kHalves, half = lane % G::kHalves;
+            const int t = u / nch, ch = u - t * nch;
+            const int row = (int)((wblk + (t == 0 ? 0 : wup) + kc + ch) * kMxChunkRows);
+            const uint32_t dst = st + G::kOffW + (t * G::kCPS + ch) * G::kCB;
+            tma_load_2d_lane(u < G::kNT * nch, dst + half * kMxCodeBytes, &tmap_w, half * 128, row, fb);
+            const int v = lane - 16, tv = v / nch, cv = v - tv * nch;   // lanes 16 and up
+            bulk_g2s_lane(v >= 0 && v < G::kNT * nch, st + G::kOffW + (tv * G::kCPS + cv) * G::kCB + G::kCBScale,
+                          (tv == 0 ? wsrc : wsrc_up) + (size_t)(kc + cv) * kPackedCB + kMxCodeBytes, 1024u, fb);
+          } else {
+            const int t = lane / nch, ch = lane - t * nch;
+            bulk_g2s_lane(lane < G::kNT * nch, st + G::kOffW + (t * G::kCPS + ch) * G::kCB,
+                          (t == 0 ? wsrc : wsrc_up) + (size_t)(kc + ch) * G::kCB, G::kCB, fb);
+          }
+          tma_load_3d_lane(lane == 31, st + G::kOffSFB, &tmap_sfb, 0, c.r0, kc * G::kSfPerChunk, fb);
         } else {
-          // activation codes: lane ch * nb + b copies box b (64-row boxes first) of chunk ch
-          mbar_arrive_expect_tx(fb, (uint32_t)(nch * rows * 128));
+          // activation codes: lane ch * nb + b copies box b (64-row boxes first) of chunk ch (of 128-byte
+          // half ch of the stage's chunks for 8-bit activations)
+          mbar_arrive_expect_tx(fb, (uint32_t)(nch * G::kHalves * rows * 128));
           const int nb = n64 + n32;
           const int ch = nb > 0 ? lane / nb : 0, b = lane - ch * nb;
           const bool b64 = b < n64;
           const int roff = b64 ? 64 * b : 64 * n64 + (b - n64) * G::kBoxH;
-          tma_load_2d_lane(lane < nch * nb, st + ch * G::kBChunk + roff * 128, b64 ? &tmap_b64 : &tmap_b,
-                           (kc + ch) * 128, r0 + roff, fb);
+          tma_load_2d_lane(lane < nch * G::kHalves * nb, st + ch * (G::kBChunk / G::kHalves) + roff * 128,
+                           b64 ? &tmap_b64 : &tmap_b, (kc * G::kHalves + ch) * 128, r0 + roff, fb);
         }
         ++g;
         if (++s == S) { s = 0; ph ^= 1u; }
@@ -851,13 +944,13 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
               }
         }
 #pragma unroll
-        for (int kb = 0; kb < G::kKbps; ++kb) {
-          if (kb < nch * G::kKbPerChunk) {
+        for (int kb = 0; kb < G::kSfps; ++kb) {
+          if (kb < nch * G::kSfPerChunk) {
 #pragma unroll
             for (int t = 0; t < G::kNT; ++t) {
-              const uint32_t sfa = st + G::kOffW + (t * G::kCPS + kb / G::kKbPerChunk) * G::kCB + G::kCBScale +
-                                   (kb % G::kKbPerChunk) * 512;
-              const int m = G::kColSFA + 4 * (t * G::kKbps + kb);
+              const uint32_t sfa = st + G::kOffW + (t * G::kCPS + kb / G::kSfPerChunk) * G::kCB + G::kCBScale +
+                                   (kb % G::kSfPerChunk) * 512;
+              const int m = G::kColSFA + 4 * (t * G::kSfps + kb);
               lds128(sfa + lane * 16, r[m], r[m + 1], r[m + 2], r[m + 3]);
             }
             lds128(st + G::kOffSFB + kb * 512 + lane * 16, r[G::kColSFB + 4 * kb], r[G::kColSFB + 4 * kb + 1],
@@ -887,7 +980,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
     const int n_mma = rank == 0u ? n_my : 0;
     for (int j = 0; j < n_mma && !*abort_flag; ++j) {
       const TileDesc c = my_tile(j, ttab, p.tcap, pref, offs, E, kBN, p.sched, tb, unit, nunits);
-      const uint32_t idesc = kNative ? make_idesc(false, kTileN, kBN)   // M = 128 tokens, N = 128 weight rows
+      const uint32_t idesc = kMx ? make_idesc_mx(kFmt == kFmtMx8, (c.valid + 15) & ~15, kTileN * kCG)
+                             : kNative ? make_idesc(false, kTileN, kBN)   // M = 128 tokens, N = 128 weight rows
                                      : make_idesc(kSparse, (c.valid + 15) & ~15, kTileN * kCG);
       if (p.stall_ns != 0ull && j == (n_mma > 1 ? 1 : 0) &&
           !wait_warp(never_bar, 0u, abort_flag, p.status, p.stall_ns))
@@ -911,17 +1005,21 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
           if (ch < nch) {
 #pragma unroll
             for (int h = 0; h < G::kKbPerChunk; ++h) {
-              const int kbi = ch * G::kKbPerChunk + h;
-              const uint64_t bdesc = smem_desc(st + ch * G::kBChunk + G::kBStep * h, 16, 1024, 2);
+              const int kbi = ch * G::kSfPerChunk + h / G::kMmaPerSf;   // scale atom
+              const uint64_t bdesc = smem_desc(st + ch * G::kBChunk + G::b_off(h), 16, 1024, 2);
               const uint32_t accum = (kc | ch | h) != 0 ? 1u : 0u;
 #pragma unroll
               for (int t = 0; t < G::kNT; ++t) {
-                const uint64_t adesc =
-                    smem_desc(st + G::kOffW + (t * G::kCPS + ch) * G::kCB + 4096u * h, 128, 256, 0);
+                const uint32_t aaddr = st + G::kOffW + (t * G::kCPS + ch) * G::kCB + G::a_off(h);
+                const uint64_t adesc = kMx ? smem_desc(aaddr, 16, 1024, 2) : smem_desc(aaddr, 128, 256, 0);
                 const uint32_t d = d_tmem + (uint32_t)(t * G::kAccStride);
-                const int kt = t * G::kKbps + kbi;
+                const int kt = t * G::kSfps + kbi;
                 const uint32_t sfa = tset + G::kColSFA + 4 * kt, sfb = tset + G::kColSFB + 4 * kbi;
-                if constexpr (kNative)   // tokens as A, weights as B: the operands and their scales swap
+                if constexpr (kMx)
+                  tc_mma_mx<kFmt == kFmtMx8, kPair>(
+                      d, adesc, bdesc, idesc | idesc_sf((h % G::kMmaPerSf) * G::kSfIdStep),
+                      accum, sfa, sfb);
+                else if constexpr (kNative)   // tokens as A, weights as B: the operands and their scales swap
                   tc_mma_dense(d, bdesc, adesc, idesc, accum, sfb, sfa);
                 else if constexpr (kSparse && kPair)
                   tc_mma_sparse_pair(d, adesc, bdesc, idesc, accum, sfa, sfb, tset + 2 * kt);
@@ -960,7 +1058,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
     // =============================== epilogue (warps 3..6, and 11..14 for wide tiles -> TMEM lane
     // quadrants 3,0,1,2)
     const int q = warp & 3;
-    const float sx = __ldg(p.x_scale);
+    const float sx = kMx ? 1.0f : __ldg(p.x_scale);
     int acc = 0;
     uint32_t aph = 0;
     for (int j = 0; j < n_my; ++j) {
@@ -1211,17 +1309,16 @@ static int g_smem_limit = 232448 - 1024;
 // tcap: capacity of the per-CTA tile table (tiles beyond it are decoded on the fly); an upper
 // bound on a CTA's tiles is ceil((ceil(R/BN) + E) * NT / grid).  cg = 2: a CTA of a pair, which
 // stages half of the tile's token rows (the geometry of Geo<..., 2>).
-static GemmPlan make_plan(bool sparse, int BN, int E, int tcap, bool glu = false, int cg = 1, bool wide = false) {
+static GemmPlan make_plan(int fmt, int BN, int E, int tcap, bool glu = false, int cg = 1, bool wide = false) {
   GemmPlan g;
   g.BN = BN;
   g.tcap = tcap;
   // weight n-tiles per tile and CTA: gate + up with the SwiGLU epilogue, two n-tile pairs for a
   // wide pair tile
   const int nt = glu || wide ? 2 : 1;
-  g.cps = stage_chunks(sparse, BN, glu, cg, wide);
-  const int kbps = g.cps * (sparse ? 2 : 4);
-  const int body =
-      g.cps * (BN / cg) * 128 + nt * g.cps * (sparse ? kSparseChunkBytes : kDenseChunkBytes) + kbps * 512;
+  g.cps = stage_chunks(fmt, BN, glu, cg, wide);
+  const int sfps = g.cps * fmt_sf_chunk(fmt);
+  const int body = g.cps * (BN / cg) * fmt_act_chunk(fmt) + nt * g.cps * fmt_w_chunk(fmt) + sfps * 512;
   g.stage = (body + 1023) / 1024 * 1024;
   // everything but the stage ring and the tile table, at its largest
   const int ostage = (wide ? 8 : 4) * (glu ? kGluStageBytes : kOutStageBytes);
@@ -1287,18 +1384,18 @@ static EncodeTiledFn get_encode_fn() {
   return fn;
 }
 
-template <bool kSparse, int kBN, bool kGLU = false, int kCG = 1, bool kNative = false, bool kWide = false>
+template <int kFmt, int kBN, bool kGLU = false, int kCG = 1, bool kNative = false, bool kWide = false>
 static cudaError_t set_attr_one(int bytes) {
-  return cudaFuncSetAttribute(grouped_gemm_kernel<kSparse, kBN, kGLU, kCG, kNative, kWide>,
+  return cudaFuncSetAttribute(grouped_gemm_kernel<kFmt, kBN, kGLU, kCG, kNative, kWide>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 // CTA pairs the device can hold at once at one CTA per SM (the pairs' SMs must share a GPC), per
-// sparse/dense; 0 when the device cannot run them (then 128-token tiles run one CTA per tile).
-static int g_pair_units[2] = {0, 0};
-static int g_wide_units[2] = {0, 0};   // the same for the wide pair tiles
+// format; 0 when the device cannot run them (then 128-token tiles run one CTA per tile).
+static int g_pair_units[4] = {0, 0, 0, 0};
+static int g_wide_units[4] = {0, 0, 0, 0};   // the same for the wide pair tiles
 
-template <bool kSparse, bool kWide = false>
+template <int kFmt, bool kWide = false>
 static int max_pairs(int smem) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
@@ -1312,7 +1409,7 @@ static int max_pairs(int smem) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, grouped_gemm_kernel<kSparse, 128, false, 2, false, kWide>, &cfg) !=
+  if (cudaOccupancyMaxActiveClusters(&n, grouped_gemm_kernel<kFmt, 128, false, 2, false, kWide>, &cfg) !=
       cudaSuccess) {
     cudaGetLastError();   // clear the error: pairs are then simply not used
     return 0;
@@ -1328,73 +1425,89 @@ cudaError_t gemm_set_smem_attrs() {
   if (e != cudaSuccess) return e;
   maxb -= 1024;   // room for the kernels' static shared memory
   g_smem_limit = maxb;
-  cudaError_t errs[16] = {set_attr_one<true, 16>(maxb),       set_attr_one<true, 32>(maxb),
-                          set_attr_one<true, 64>(maxb),       set_attr_one<true, 128>(maxb),
-                          set_attr_one<false, 16>(maxb),      set_attr_one<false, 32>(maxb),
-                          set_attr_one<false, 64>(maxb),      set_attr_one<false, 128>(maxb),
-                          set_attr_one<true, 16, true>(maxb), set_attr_one<true, 32, true>(maxb),
-                          set_attr_one<true, 64, true>(maxb), set_attr_one<true, 128, false, 2>(maxb),
-                          set_attr_one<false, 128, false, 2>(maxb), set_attr_one<false, 128, false, 1, true>(maxb),
-                          set_attr_one<true, 128, false, 2, false, true>(maxb),
-                          set_attr_one<false, 128, false, 2, false, true>(maxb)};
+  constexpr int D = kFmtDense, S = kFmtSparse, M4 = kFmtMx4, M8 = kFmtMx8;
+  const cudaError_t errs[] = {
+      set_attr_one<S, 16>(maxb), set_attr_one<S, 32>(maxb), set_attr_one<S, 64>(maxb), set_attr_one<S, 128>(maxb),
+      set_attr_one<D, 16>(maxb), set_attr_one<D, 32>(maxb), set_attr_one<D, 64>(maxb), set_attr_one<D, 128>(maxb),
+      set_attr_one<S, 16, true>(maxb), set_attr_one<S, 32, true>(maxb), set_attr_one<S, 64, true>(maxb),
+      set_attr_one<S, 128, false, 2>(maxb), set_attr_one<D, 128, false, 2>(maxb),
+      set_attr_one<D, 128, false, 1, true>(maxb), set_attr_one<S, 128, false, 2, false, true>(maxb),
+      set_attr_one<D, 128, false, 2, false, true>(maxb),
+      set_attr_one<M4, 16>(maxb), set_attr_one<M4, 32>(maxb), set_attr_one<M4, 64>(maxb), set_attr_one<M4, 128>(maxb),
+      set_attr_one<M8, 16>(maxb), set_attr_one<M8, 32>(maxb), set_attr_one<M8, 64>(maxb),
+      set_attr_one<M4, 128, false, 2>(maxb), set_attr_one<M8, 128, false, 2>(maxb),
+      set_attr_one<M4, 128, false, 2, false, true>(maxb)};
   for (cudaError_t x : errs)
     if (x != cudaSuccess) return x;
-  g_pair_units[1] = max_pairs<true>(maxb);
-  g_pair_units[0] = max_pairs<false>(maxb);
-  g_wide_units[1] = max_pairs<true, true>(maxb);
-  g_wide_units[0] = max_pairs<false, true>(maxb);
+  g_pair_units[S] = max_pairs<S>(maxb);
+  g_pair_units[D] = max_pairs<D>(maxb);
+  g_pair_units[M4] = max_pairs<M4>(maxb);
+  g_pair_units[M8] = max_pairs<M8>(maxb);
+  g_wide_units[S] = max_pairs<S, true>(maxb);
+  g_wide_units[D] = max_pairs<D, true>(maxb);
+  g_wide_units[M4] = max_pairs<M4, true>(maxb);   // (8-bit activations: a wide stage leaves room for two only)
   return cudaSuccess;
 }
 
-template <bool kSparse, bool kGLU = false>
+template <int kFmt, bool kGLU = false>
 static cudaError_t launch_bn(int BN, int grid, size_t smem, cudaStream_t stream, const CUtensorMap& tb,
-                             const CUtensorMap& tb64, const CUtensorMap& ts, const GemmParams& p) {
+                             const CUtensorMap& tb64, const CUtensorMap& ts, const CUtensorMap& tw,
+                             const GemmParams& p) {
   switch (BN) {
-    case 16: return launch_pdl(grouped_gemm_kernel<kSparse, 16, kGLU, 1>, grid, kGemmThreads, smem, stream, tb, tb64, ts, p);
-    case 32: return launch_pdl(grouped_gemm_kernel<kSparse, 32, kGLU, 1>, grid, kGemmThreads, smem, stream, tb, tb64, ts, p);
-    default: return launch_pdl(grouped_gemm_kernel<kSparse, 64, kGLU, 1>, grid, kGemmThreads, smem, stream, tb, tb64, ts, p);
+    case 16: return launch_pdl(grouped_gemm_kernel<kFmt, 16, kGLU, 1>, grid, kGemmThreads, smem, stream, tb, tb64, ts, tw, p);
+    case 32: return launch_pdl(grouped_gemm_kernel<kFmt, 32, kGLU, 1>, grid, kGemmThreads, smem, stream, tb, tb64, ts, tw, p);
+    default: return launch_pdl(grouped_gemm_kernel<kFmt, 64, kGLU, 1>, grid, kGemmThreads, smem, stream, tb, tb64, ts, tw, p);
   }
 }
 
-template <bool kSparse>
-static cudaError_t launch_bn(int BN, int grid, size_t smem, cudaStream_t stream, const CUtensorMap& tb,
-                             const CUtensorMap& tb64, const CUtensorMap& ts, const GemmParams& p, bool glu,
-                             bool pair, bool native = false, bool wide = false) {
-  if (glu) return launch_bn<true, true>(BN, grid, smem, stream, tb, tb64, ts, p);
-  if (!kSparse && native)
-    return launch_pdl(grouped_gemm_kernel<false, 128, false, 1, true>, grid, kGemmThreads, smem, stream, tb, tb64, ts,
-                      p);
-  if (BN == 128 && pair && wide)
-    return launch_pdl_cluster(grouped_gemm_kernel<kSparse, 128, false, 2, false, true>, grid, kGemmThreadsWide, smem,
-                              stream, 2u, tb, tb64, ts, p);
+template <int kFmt>
+static cudaError_t launch_fmt(int BN, int grid, size_t smem, cudaStream_t stream, const CUtensorMap& tb,
+                              const CUtensorMap& tb64, const CUtensorMap& ts, const CUtensorMap& tw,
+                              const GemmParams& p, bool glu, bool pair, bool native, bool wide) {
+  if constexpr (kFmt == kFmtSparse)
+    if (glu) return launch_bn<kFmt, true>(BN, grid, smem, stream, tb, tb64, ts, tw, p);
+  if constexpr (kFmt == kFmtDense)
+    if (native)
+      return launch_pdl(grouped_gemm_kernel<kFmt, 128, false, 1, true>, grid, kGemmThreads, smem, stream, tb, tb64, ts,
+                        tw, p);
+  if constexpr (kFmt != kFmtMx8)
+    if (BN == 128 && pair && wide)
+      return launch_pdl_cluster(grouped_gemm_kernel<kFmt, 128, false, 2, false, true>, grid, kGemmThreadsWide, smem,
+                                stream, 2u, tb, tb64, ts, tw, p);
   if (BN == 128 && pair)
-    return launch_pdl_cluster(grouped_gemm_kernel<kSparse, 128, false, 2>, grid, kGemmThreads, smem, stream, 2u, tb,
-                              tb64, ts, p);
-  if (BN == 128)
-    return launch_pdl(grouped_gemm_kernel<kSparse, 128, false, 1>, grid, kGemmThreads, smem, stream, tb, tb64, ts, p);
-  return launch_bn<kSparse, false>(BN, grid, smem, stream, tb, tb64, ts, p);
+    return launch_pdl_cluster(grouped_gemm_kernel<kFmt, 128, false, 2>, grid, kGemmThreads, smem, stream, 2u, tb,
+                              tb64, ts, tw, p);
+  if constexpr (kFmt != kFmtMx8)
+    if (BN == 128)
+      return launch_pdl(grouped_gemm_kernel<kFmt, 128, false, 1>, grid, kGemmThreads, smem, stream, tb, tb64, ts, tw,
+                        p);
+  return launch_bn<kFmt, false>(BN, grid, smem, stream, tb, tb64, ts, tw, p);
 }
 
 // returns 0 ok, 1 cuda error, 2 tensor map failure.  h_scales / h_scale non-null: the SwiGLU
 // epilogue (sparse only; Y receives the h codes).  comb non-null: the combine epilogue (Y is the
 // slot buffer, bf16 output only).
-int launch_gemm(bool sparse, const uint8_t* a_codes, const uint8_t* a_scales, const float* x_scale,
+int launch_gemm(int fmt, const uint8_t* a_codes, const uint8_t* a_scales, const float* x_scale,
                 const uint8_t* w_packed, const float* w_scale, const int32_t* off, int E, int N, int K, int R,
                 int max_rows, void* Y, int y_f32, int* status, int num_sms, cudaStream_t stream,
                 uint8_t* h_scales, const float* h_scale, const CombineArgs* comb, bool native) {
   EncodeTiledFn enc = get_encode_fn();
   if (enc == nullptr) return 2;
   const bool glu = h_scales != nullptr;
-  if (native && (sparse || glu || comb != nullptr)) return 1;
+  if (native && (fmt != kFmtDense || glu || comb != nullptr)) return 1;
+  if ((glu || comb != nullptr) && fmt != kFmtSparse) return 1;
   int BN = native ? 128 : gemm_pick_bn(max_rows, R, E);   // the native orientation: 128-token tiles (MMA M)
   if (glu && BN > 64) BN = 64;   // two accumulators per tile: 64-token tiles at most
+  // 8-bit activations: 128-token tiles only on CTA pairs (one CTA's 66 KB stage leaves room for two, and
+  // the TMEM sets need three)
+  if (fmt == kFmtMx8 && BN == 128 && ((N / kTileN) % 2 != 0 || g_pair_units[fmt] == 0)) BN = 64;
   // 128-token tiles run as CTA pairs (256 weight rows per tile) when N holds whole n-tile pairs
   // and the device can co-schedule pairs
   // a wide pair tile (no combine epilogue, N a multiple of 512) holds two n-tile pairs, 512 weight
   // rows, and reads its 128 tokens' activations once for both
   const bool wide = BN == 128 && !glu && !native && comb == nullptr && (N / kTileN) % 4 == 0 &&
-                    g_wide_units[sparse ? 1 : 0] > 0;
-  const int pair_units = wide ? g_wide_units[sparse ? 1 : 0] : g_pair_units[sparse ? 1 : 0];
+                    g_wide_units[fmt] > 0;
+  const int pair_units = wide ? g_wide_units[fmt] : g_pair_units[fmt];
   const bool pair = BN == 128 && !glu && !native && (N / kTileN) % 2 == 0 && pair_units > 0;
   const int cg = pair ? 2 : 1;
   const int units = pair ? (pair_units < num_sms / 2 ? pair_units : num_sms / 2) : num_sms;   // pairs or CTAs
@@ -1411,8 +1524,8 @@ int launch_gemm(bool sparse, const uint8_t* a_codes, const uint8_t* a_scales, co
   long long tcap;
   if (sched == kSchedRuns) {
     // a CTA's share of the bytes holds at most (wc + BN ac) / (wc + ac) times the average tile count
-    const long long wc = (glu ? 2LL : 1LL) * kTileN * K * (sparse ? 11 : 18) / 32;
-    const long long ac = K / 2 + K / (sparse ? 32 : 16) + (glu ? 2LL : 1LL) * kTileN * (y_f32 ? 4 : 2);
+    const long long wc = (glu ? 2LL : 1LL) * kTileN * K * fmt_w_bytes32(fmt) / 32;
+    const long long ac = fmt_act_row(fmt, K) + (glu ? 2LL : 1LL) * kTileN * (y_f32 ? 4 : 2);
     tcap = (bound * (wc + BN * ac) / (wc + ac) + units - 1) / units + 2;
   } else {
     tcap = (bound + units - 1) / units;
@@ -1420,18 +1533,19 @@ int launch_gemm(bool sparse, const uint8_t* a_codes, const uint8_t* a_scales, co
   if (tcap > kMaxTableTiles) tcap = kMaxTableTiles;
   const int tcap_test = g_test_table_cap.load();
   if (tcap_test >= 0 && tcap > tcap_test) tcap = tcap_test;
-  const GemmPlan g = make_plan(sparse, BN, E, (int)tcap, glu, cg, pair && wide);
+  const GemmPlan g = make_plan(fmt, BN, E, (int)tcap, glu, cg, pair && wide);
   if (g.stages < kNSets || g.smem > (size_t)g_smem_limit) return 1;   // ring too shallow: refuse, launch nothing
   const int box_h = g.BN / cg < 32 ? g.BN / cg : 32;
-  const int kbps = g.cps * (sparse ? 2 : 4);
-  const int rcap = R + kActScalePadRows;
-  const int KBa = K / (sparse ? 128 : 64);
-  CUtensorMap tb, tb64, ts;
-  // activation codes [R][K/2]: boxes of 128 bytes x box_h rows, and (token tiles >= 64) x 64 rows
+  const int sfps = g.cps * fmt_sf_chunk(fmt);
+  const int rcap = R + (fmt_mx(fmt) ? 0 : kActScalePadRows);   // (TMA boxes past the last row read zeros)
+  const int KBa = K / 256 * fmt_sf_chunk(fmt);
+  const cuuint64_t row_bytes = (cuuint64_t)(K / 256) * fmt_act_chunk(fmt);
+  CUtensorMap tb, tb64, ts, tw;
+  // activation codes [R][K/2] ([R][K] for 8-bit activations): boxes of 128 bytes x box_h rows, and (token tiles >= 64) x 64 rows
   for (int m = 0; m < 2; ++m) {
     if (m == 1 && g.BN / cg < 64) { tb64 = tb; break; }
-    cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)R};
-    cuuint64_t strides[1] = {(cuuint64_t)(K / 2)};
+    cuuint64_t dims[2] = {row_bytes, (cuuint64_t)R};
+    cuuint64_t strides[1] = {row_bytes};
     cuuint32_t box[2] = {128u, (cuuint32_t)(m == 0 ? box_h : 64)};
     cuuint32_t estr[2] = {1u, 1u};
     if (enc(m == 0 ? &tb : &tb64, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a_codes), dims, strides,
@@ -1443,12 +1557,29 @@ int launch_gemm(bool sparse, const uint8_t* a_codes, const uint8_t* a_scales, co
     // activation scale quad entries as a [KBa][rcap][16 B] tensor; one box = the stage's atoms
     cuuint64_t dims[3] = {16u, (cuuint64_t)rcap, (cuuint64_t)KBa};
     cuuint64_t strides[2] = {16u, (cuuint64_t)rcap * 16u};
-    cuuint32_t box[3] = {16u, 32u, (cuuint32_t)kbps};
+    cuuint32_t box[3] = {16u, 32u, (cuuint32_t)sfps};
     cuuint32_t estr[3] = {1u, 1u, 1u};
     if (enc(&ts, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(a_scales), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return 2;
+  }
+  if (fmt_mx(fmt)) {
+    // microscaled weights as rows of 128 bytes (256 codes): a chunk block is 128 rows of codes and 8 of
+    // scales (copied separately); one box = the codes of a block, or for 8-bit activations half of each
+    // row, which the copy widens to 16 bytes per 16 codes
+    const bool m8 = fmt == kFmtMx8;
+    cuuint64_t dims[2] = {m8 ? 256u : 128u, (cuuint64_t)E * (N / kTileN) * (K / kChunkK) * kMxChunkRows};
+    cuuint64_t strides[1] = {128u};
+    cuuint32_t box[2] = {128u, 128u};
+    cuuint32_t estr[2] = {1u, 1u};
+    if (enc(&tw, m8 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+            const_cast<uint8_t*>(w_packed), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
+        CUDA_SUCCESS)
+      return 2;
+  } else {
+    tw = ts;   // not read
   }
   GemmParams p;
   p.a_scales = a_scales; p.x_scale = x_scale; p.w_packed = w_packed;
@@ -1462,8 +1593,13 @@ int launch_gemm(bool sparse, const uint8_t* a_codes, const uint8_t* a_scales, co
   p.out = comb ? comb->out : nullptr;
   p.k = comb ? comb->k : 1;
   p.stall_ns = g_test_stall_ns.load();
-  const cudaError_t e = sparse ? launch_bn<true>(g.BN, grid, g.smem, stream, tb, tb64, ts, p, glu, pair, false, wide)
-                               : launch_bn<false>(g.BN, grid, g.smem, stream, tb, tb64, ts, p, false, pair, native, wide);
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (fmt) {
+    case kFmtDense: e = launch_fmt<kFmtDense>(g.BN, grid, g.smem, stream, tb, tb64, ts, tw, p, glu, pair, native, wide); break;
+    case kFmtSparse: e = launch_fmt<kFmtSparse>(g.BN, grid, g.smem, stream, tb, tb64, ts, tw, p, glu, pair, native, wide); break;
+    case kFmtMx4: e = launch_fmt<kFmtMx4>(g.BN, grid, g.smem, stream, tb, tb64, ts, tw, p, glu, pair, native, wide); break;
+    case kFmtMx8: e = launch_fmt<kFmtMx8>(g.BN, grid, g.smem, stream, tb, tb64, ts, tw, p, glu, pair, native, wide); break;
+  }
   return e == cudaSuccess ? 0 : 1;
 }
 

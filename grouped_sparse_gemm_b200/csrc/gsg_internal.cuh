@@ -24,6 +24,11 @@ constexpr int kChunkK = 256;           // logical K per pipeline stage / metadat
 constexpr int kActScalePadRows = 256;  // extra zero rows of the quad activation-scale layout
 constexpr int kSparseChunkBytes = 11264;  // packed weight chunk block: values 8192 | meta 2048 | scales 1024
 constexpr int kDenseChunkBytes = 18432;   // dense control chunk block: codes 16384 | scales 2048
+// microscaled (MXFP4) chunk block: 128 rows of 256 codes, then the two 512-byte scale atoms of its two
+// 128-wide k-blocks; 136 rows of 128 bytes
+constexpr int kMxCodeBytes = 16384;
+constexpr int kMxChunkBytes = 17408;
+constexpr int kMxChunkRows = 136;
 constexpr float kTensorScaleDen = 2688.0f;  // 6 * 448
 
 // ------------------------------------------------------------------ status word

@@ -30,6 +30,18 @@ cudaError_t launch_quant(const uint16_t* X, int T, int K, int sf, const int32_t*
                          uint8_t* codes, uint8_t* scales, float* s_out, float* partial, int partials_ready,
                          uint32_t* raw, int* status, int num_sms, cudaStream_t stream);
 
+// Row-major scale words raw [R][KBa] -> the quad layout [KBa][rcap][4] (0 past row R).
+cudaError_t launch_scales_quad(const uint32_t* raw, int R, int KBa, int rcap, uint32_t* quad, cudaStream_t stream);
+
+// gsg_mx.cu
+cudaError_t launch_pack_mxfp4(const void* W, bool w_f32, int E, int N, int K, uint8_t* packed, int* status,
+                              cudaStream_t stream);
+cudaError_t launch_pack_mxfp4_codes(const uint8_t* codes, const uint8_t* scales, int E, int N, int K, uint8_t* packed,
+                                    int* status, cudaStream_t stream);
+// bits: 4 or 8; raw: workspace of quant_raw_bytes(T*k, K) bytes for the two-phase scale path (nullptr: direct)
+cudaError_t launch_quant_mx(const uint16_t* X, int T, int K, int bits, const int32_t* inv_perm, int k, uint8_t* codes,
+                            uint8_t* scales, uint32_t* raw, int* status, int num_sms, cudaStream_t stream);
+
 // gsg_route.cu
 int route_chunks(int R, int E);
 size_t route_workspace_bytes(int R, int E);
@@ -57,6 +69,11 @@ struct CombineArgs {          // the combine epilogue of the down-projection
   uint16_t* out;              // [T][N] bf16
   int k;
 };
+// operand formats of the grouped GEMM
+constexpr int kGemmDense = 0;    // NVFP4, dense weights (the control)
+constexpr int kGemmSparse = 1;   // NVFP4, paired 4:8 weights
+constexpr int kGemmMx4 = 2;      // MXFP4 weights, MXFP4 activations
+constexpr int kGemmMx8 = 3;      // MXFP4 weights, MXFP8 (E4M3) activations
 bool gemm_supported(int E);
 // test hook: GEMM launches after this call stall their MMA warp for `ns` on a barrier nothing
 // arrives on (0 = off); see GemmParams::stall_ns
@@ -65,7 +82,7 @@ void gemm_set_test_stall(unsigned long long ns);
 void gemm_set_test_table_cap(int cap);
 int gemm_pick_bn(int max_rows, int R, int E);
 cudaError_t gemm_set_smem_attrs();
-int launch_gemm(bool sparse, const uint8_t* a_codes, const uint8_t* a_scales, const float* x_scale,
+int launch_gemm(int fmt, const uint8_t* a_codes, const uint8_t* a_scales, const float* x_scale,
                 const uint8_t* w_packed, const float* w_scale, const int32_t* off, int E, int N, int K, int R,
                 int max_rows, void* Y, int y_f32, int* status, int num_sms, cudaStream_t stream,
                 uint8_t* h_scales = nullptr, const float* h_scale = nullptr, const CombineArgs* comb = nullptr,

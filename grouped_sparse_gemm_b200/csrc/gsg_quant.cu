@@ -318,6 +318,11 @@ act_quant_kernel(QuantParams p) {
   quant_zero_padding(p);
 }
 
+cudaError_t launch_scales_quad(const uint32_t* raw, int R, int KBa, int rcap, uint32_t* quad, cudaStream_t stream) {
+  const dim3 grid((unsigned)ceil_div_i(rcap, kQuadTileRows), (unsigned)ceil_div_i(KBa, kQuadTileKb));
+  return launch_pdl(act_scales_quad_kernel, grid, 256, 0, stream, raw, R, KBa, rcap, quad);
+}
+
 size_t quant_raw_offset(long long n_elems) {
   return ((size_t)quant_partials(n_elems) * sizeof(float) + 255) / 256 * 256;
 }
@@ -360,10 +365,7 @@ cudaError_t launch_quant(const uint16_t* X, int T, int K, int sf, const int32_t*
   if (sf == 32) {
     cudaError_t e = launch_pdl(act_quant32_kernel, (unsigned)blocks, kQuantMainThreads, 0, stream, p);
     if (e != cudaSuccess || p.raw == nullptr) return e;
-    const int KBa = K / 128;
-    const dim3 grid((unsigned)ceil_div_i(p.rcap, kQuadTileRows), (unsigned)ceil_div_i(KBa, kQuadTileKb));
-    return launch_pdl(act_scales_quad_kernel, grid, 256, 0, stream, (const uint32_t*)p.raw, p.R, KBa, p.rcap,
-                      reinterpret_cast<uint32_t*>(scales));
+    return launch_scales_quad(p.raw, p.R, K / 128, p.rcap, reinterpret_cast<uint32_t*>(scales), stream);
   }
   return launch_pdl(act_quant_kernel, (unsigned)blocks, kQuantMainThreads, 0, stream, p);
 }

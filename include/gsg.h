@@ -71,11 +71,15 @@ enum {
   GSG_OP_QUANTIZE = 4,
   GSG_OP_GEMM = 5,
   GSG_OP_COMBINE = 6,   /* gsg_grouped_sparse_gemm_combine: token slots + barrier counters    */
-  GSG_OP_DISPATCH = 7   /* gsg_moe_dispatch_nvfp4: routing workspace + quantizer workspace    */
+  GSG_OP_DISPATCH = 7,  /* gsg_moe_dispatch_nvfp4: routing workspace + quantizer workspace    */
+  GSG_OP_QUANTIZE_MX = 8 /* gsg_quantize_act_mx                                               */
 };
 
-/* Output element types of the grouped GEMMs. */
+/* Output element types of the grouped GEMMs (and the element types of the calls that take either). */
 enum { GSG_OUT_BF16 = 0, GSG_OUT_F32 = 1 };
+
+/* Microscaled element formats: E2M1 or E4M3 codes with one UE8M0 scale per 32 values. */
+enum { GSG_MXFP4 = 4, GSG_MXFP8 = 8 };
 
 /* ----------------------------------------------------------------------------------------
  * Buffer sizes in bytes (host-only arithmetic, no GPU access).
@@ -258,6 +262,57 @@ gsg_status_t gsg_grouped_sparse_gemm_combine(const uint8_t* a_codes, const uint8
                                              int max_rows_per_expert, const int32_t* perm_src,
                                              const float* gates, void* workspace, size_t workspace_bytes,
                                              uint16_t* out, void* stream);
+
+/* ----------------------------------------------------------------------------------------
+ * Microscaled (OCP MX) experts.  The paper has no counterpart: these calls run the same routed layer on
+ * the weight format that published mixture-of-experts checkpoints use, dense MXFP4, with activations in
+ * MXFP4 or MXFP8.  A block is 32 consecutive values along K: one scale 2^e, stored as the byte e + 127
+ * (UE8M0), and 32 codes, E2M1 (MXFP4, low nibble = even k) or E4M3 (MXFP8).  With b the block's largest
+ * magnitude, e = clamp(floor(log2 b) - emax, -127, 127), emax = 2 for E2M1 and 8 for E4M3 (e = -127 when
+ * b = 0), code = v / 2^e rounded to nearest even, saturating.  There is no tensor scale.
+ * Packed weights: for expert e, n-tile nt and 256-wide K chunk kc, one block of 17408 bytes at
+ * ((e*NT + nt)*(K/256) + kc) * 17408:
+ *   codes  r*128 + c for row r (0..127) of the n-tile and byte c of the chunk's 256 codes of that row.
+ *   scales 16384 + h*512 + 16*(r%32) + 4*(r/32) + j for 32-block 4*h + j of the chunk.
+ * 4.25 bit/weight.  w_packed must be 128-byte aligned.  E <= 1024 and E*N*K*17/4096 < 2^31 (rows of 128
+ * bytes), else GSG_ERR_UNSUPPORTED_SHAPE.
+ * Activations: codes [R][K/2] (MXFP4) or [R][K] (MXFP8); scales [K/128][R][4][4 B], entry (kb, r, c, j) =
+ * scale byte of block 4*kb + j of row r + 32*c (0 when r + 32*c >= R): the quad layout above without its
+ * padding rows.
+ */
+size_t gsg_mx_packed_bytes(int E, int N, int K);             /* E*N*K*17/32 (4.25 bit)     */
+size_t gsg_mx_act_codes_bytes(int R, int K, int fmt);        /* R*K*fmt/8                  */
+size_t gsg_mx_act_scales_bytes(int R, int K);                /* K/128 * R * 16             */
+
+/* gsg_pack_mxfp4 -- quantize and pack W [E][N][K] (w_dtype GSG_OUT_BF16 or GSG_OUT_F32).  Non-finite W
+ * sets GSG_ERR_NONFINITE.  No workspace. */
+gsg_status_t gsg_pack_mxfp4(const void* W, int w_dtype, int E, int N, int K, uint8_t* w_packed, void* stream);
+
+/* gsg_pack_mxfp4_codes -- pack weights that are MXFP4 already: codes [E][N][K/2] (low nibble = even k) and
+ * scale bytes [E][N][K/32], as checkpoints store them.  The values are not changed.  A scale byte of 0xFF
+ * (NaN) sets GSG_ERR_NONFINITE. */
+gsg_status_t gsg_pack_mxfp4_codes(const uint8_t* codes, const uint8_t* scales, int E, int N, int K,
+                                  uint8_t* w_packed, void* stream);
+
+/* gsg_quantize_act_mx -- activations X bf16 [T][K] to MXFP4 or MXFP8 (fmt), each token quantized once and
+ * written to its k routed rows inv_perm[t*k + j] (inv_perm NULL: row t, and k must be 1).  R = T*k rows.
+ * Non-finite X sets GSG_ERR_NONFINITE, a routed row outside [0, R) GSG_ERR_BAD_ROUTING.  K % 256 == 0,
+ * T*k <= 2^30, T*K/16 < 2^31, else GSG_ERR_UNSUPPORTED_SHAPE.
+ * workspace: gsg_workspace_size(GSG_OP_QUANTIZE_MX, 0, 0, K, T, k) bytes, 16-byte aligned (0 below
+ * R*K = 2^27: then it may be NULL). */
+gsg_status_t gsg_quantize_act_mx(const uint16_t* X, int T, int K, int fmt, const int32_t* inv_perm, int k,
+                                 uint8_t* codes, uint8_t* scales, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* gsg_grouped_mx_gemm -- for each expert e and routed row r in [off[e], off[e+1]):
+ *     Y[r][n] = sum_k a[r][k] * w[e][n][k]      (fp32 accumulation)
+ * a_codes / a_scales in act_fmt from gsg_quantize_act_mx or gsg_add_rmsnorm_mx, w_packed from
+ * gsg_pack_mxfp4 or gsg_pack_mxfp4_codes.  Everything else (offsets, the max_rows_per_expert hint, Y, rows
+ * that are not written) as for gsg_grouped_sparse_gemm.  E = 1 with offsets {0, R} is a plain linear layer.
+ * No workspace. */
+gsg_status_t gsg_grouped_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int act_fmt,
+                                 const uint8_t* w_packed, const int32_t* expert_offsets, int E, int N, int K, int R,
+                                 int max_rows_per_expert, void* Y, int y_dtype, void* stream);
 
 /* ----------------------------------------------------------------------------------------
  * gsg_unpermute_scale -- gate-weighted scatter back to tokens.
