@@ -31,7 +31,7 @@ __all__ = [
     "grouped_dense_gemm", "grouped_dense_gemm_native", "unpermute_scale", "OP_COMBINE", "OP_DISPATCH",
     "get_device_status",
     "PackedMxWeights", "MxActivations", "pack_mxfp4", "pack_mxfp4_codes", "quantize_act_mx", "grouped_mx_gemm",
-    "OP_QUANTIZE_MX", "MXFP4", "MXFP8",
+    "OP_QUANTIZE_MX", "MXFP4", "MXFP8", "moe_gate", "NormOutput", "add_rmsnorm_mx",
     "save_packed", "load_packed",
     "act_scales_bytes", "workspace_size", "OP_PACK_SPARSE", "OP_PACK_DENSE", "OP_ROUTE",
     "OP_QUANTIZE", "OP_GEMM", "EXPORTED_SYMBOLS",
@@ -53,7 +53,7 @@ EXPORTED_SYMBOLS = [
     "gsg_moe_dispatch_nvfp4", "gsg_test_set_gemm_stall_ns", "gsg_grouped_dense_gemm_native",
     "gsg_test_set_gemm_table_cap",
     "gsg_mx_packed_bytes", "gsg_mx_act_codes_bytes", "gsg_mx_act_scales_bytes", "gsg_pack_mxfp4",
-    "gsg_pack_mxfp4_codes", "gsg_quantize_act_mx", "gsg_grouped_mx_gemm",
+    "gsg_pack_mxfp4_codes", "gsg_quantize_act_mx", "gsg_grouped_mx_gemm", "gsg_moe_gate", "gsg_add_rmsnorm_mx",
 ]
 
 _STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported shape", -3: "CUDA error",
@@ -114,6 +114,8 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         "gsg_pack_mxfp4": (i, [vp, i, i, i, i, vp, vp]),
         "gsg_pack_mxfp4_codes": (i, [vp, vp, i, i, i, vp, vp]),
         "gsg_quantize_act_mx": (i, [vp, i, i, i, vp, i, vp, vp, vp, sz, vp]),
+        "gsg_moe_gate": (i, [vp, i, vp, i, i, i, i, i, i, i, i, ctypes.c_float, vp, vp, vp]),
+        "gsg_add_rmsnorm_mx": (i, [vp, vp, i, vp, i, i, i, ctypes.c_float, vp, vp, i, vp, vp, vp]),
         "gsg_grouped_mx_gemm": (i, [vp, vp, i, vp, vp, i, i, i, i, i, vp, i, vp]),
     }
     for name, (res, args) in sig.items():
@@ -249,6 +251,13 @@ class MxActivations:
     R: int
     K: int
     fmt: int                # MXFP4 (4) or MXFP8 (8)
+
+
+@dataclass
+class NormOutput:
+    act: Optional[MxActivations]   # microscaled rows (None when fmt is None)
+    y: Optional[torch.Tensor]      # bf16 [T, K] (None when not wanted)
+    h: Optional[torch.Tensor]      # [T, K], the residual stream after the addition (None without a residual)
 
 
 # ------------------------------------------------------------------ storage
@@ -512,7 +521,7 @@ def grouped_dense_gemm_native(act: QuantizedActivations, w: PackedDenseWeights, 
     return out
 
 
-# ------------------------------------------------------------------ microscaled experts
+# ------------------------------------------------------------------ router, norm, microscaled experts
 def _args(stream, *ts: Optional[torch.Tensor]) -> int:
     """The checks of the tensors of one call (CUDA, contiguous, on the current device, where the kernels
     run) and the stream to launch on."""
@@ -561,6 +570,62 @@ def _mx_weights(out: Optional[PackedMxWeights], E: int, N: int, K: int, device) 
         raise ValueError(f"out: E={out.E} N={out.N} K={out.K}, expected E={E} N={N} K={K}")
     packed = _out(None if out is None else out.packed, (n,), torch.uint8, device, "packed")
     return out if out is not None else PackedMxWeights(packed, E, N, K)
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def moe_gate(logits: torch.Tensor, top_k: int, scoring: str = "softmax", bias: Optional[torch.Tensor] = None,
+             n_group: int = 1, topk_group: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+             out_ids: Optional[torch.Tensor] = None, out_gates: Optional[torch.Tensor] = None, stream=None):
+    """Router logits bf16 or fp32 [T, E] -> (topk ids int32 [T, top_k], gates fp32 [T, top_k]), as the routing
+    calls and unpermute_scale take them (gsg_moe_gate)."""
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"logits: fp32 or bf16 [T, E] wanted, got {logits.dtype} {tuple(logits.shape)}")
+    if scoring not in _SCORES:
+        raise ValueError(f"scoring {scoring!r}: 'softmax' or 'sigmoid'")
+    T, E = logits.shape
+    if bias is not None and (bias.dtype != torch.float32 or bias.numel() != E):
+        raise ValueError(f"bias: fp32 of {E} entries wanted")
+    s = _args(stream, logits, bias, out_ids, out_gates)
+    out_ids = _out(out_ids, (T, top_k), torch.int32, logits.device, "out_ids")
+    out_gates = _out(out_gates, (T, top_k), torch.float32, logits.device, "out_gates")
+    _check("gsg_moe_gate", lib().gsg_moe_gate(
+        logits.data_ptr(), OUT_F32 if logits.dtype == torch.float32 else OUT_BF16, _ptr_of(bias), T, E, top_k,
+        _SCORES[scoring], n_group, topk_group, group_top, 1 if renormalize else 0, scale, out_ids.data_ptr(),
+        out_gates.data_ptr(), s))
+    return out_ids, out_gates
+
+
+def add_rmsnorm_mx(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   fmt: Optional[int] = MXFP8, want_y: bool = True, out_act: Optional[MxActivations] = None,
+                   out_y: Optional[torch.Tensor] = None, out_h: Optional[torch.Tensor] = None,
+                   stream=None) -> NormOutput:
+    """h = x + residual, y = rmsnorm(h) * weight; y in bf16 (want_y) and in MXFP8 or MXFP4 (fmt, None: not)
+    from one pass (gsg_add_rmsnorm_mx).  x bf16 [T, K], residual bf16 or fp32 (out_h may be the residual
+    itself), weight bf16 or fp32 [K]."""
+    if x.dim() != 2 or x.dtype != torch.bfloat16:
+        raise ValueError(f"x: bf16 [T, K] wanted, got {x.dtype} {tuple(x.shape)}")
+    T, K = x.shape
+    if weight.numel() != K or weight.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"weight: fp32 or bf16 of {K} entries wanted")
+    s = _args(stream, x, weight, residual, out_y, out_h, None if out_act is None else out_act.codes,
+              None if out_act is None else out_act.scales)
+    h = y = act = None
+    if residual is not None:
+        if residual.shape != x.shape or residual.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"residual: fp32 or bf16 {tuple(x.shape)} wanted")
+        h = _out(out_h, (T, K), residual.dtype, x.device, "out_h")
+    if want_y or out_y is not None:
+        y = _out(out_y, (T, K), torch.bfloat16, x.device, "out_y")
+    if fmt is not None:
+        act = _mx_activations(out_act, T, K, fmt, x.device)
+    _check("gsg_add_rmsnorm_mx", lib().gsg_add_rmsnorm_mx(
+        x.data_ptr(), _ptr_of(residual), OUT_F32 if h is not None and h.dtype == torch.float32 else OUT_BF16,
+        weight.data_ptr(), OUT_F32 if weight.dtype == torch.float32 else OUT_BF16, T, K, eps, _ptr_of(h), _ptr_of(y),
+        0 if fmt is None else fmt, None if act is None else act.codes.data_ptr(),
+        None if act is None else act.scales.data_ptr(), s))
+    return NormOutput(act, y, h)
 
 
 def pack_mxfp4(W: torch.Tensor, out: Optional[PackedMxWeights] = None, stream=None) -> PackedMxWeights:

@@ -11,7 +11,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libgsg.so")
 SOURCES = ["gsg_api.cu", "gsg_pack.cu", "gsg_quant.cu", "gsg_route.cu", "gsg_unpermute.cu", "gsg_gemm.cu",
-           "gsg_noalloc.cu", "gsg_mx.cu"]
+           "gsg_noalloc.cu", "gsg_mx.cu", "gsg_gate.cu", "gsg_norm.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

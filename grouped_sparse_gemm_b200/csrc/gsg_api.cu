@@ -275,6 +275,48 @@ gsg_status_t gsg_quantize_act_mx(const uint16_t* X, int T, int K, int fmt, const
                                         as_stream(stream)));
 }
 
+gsg_status_t gsg_moe_gate(const void* logits, int logits_dtype, const float* bias, int T, int E, int k, int scoring,
+                          int n_group, int topk_group, int group_top, int renormalize, float scale,
+                          int32_t* topk_ids, float* gates, void* stream) {
+  if (T < 0 || k < 1 || E < 1 || (logits_dtype != GSG_OUT_BF16 && logits_dtype != GSG_OUT_F32) ||
+      (scoring != GSG_SCORE_SOFTMAX && scoring != GSG_SCORE_SIGMOID))
+    return GSG_ERR_INVALID_ARG;
+  if (E > 1024 || k > 32 || n_group > 32 || (long long)T * E >= (1ll << 40)) return GSG_ERR_UNSUPPORTED_SHAPE;
+  if (n_group < 1 || E % n_group != 0 || topk_group < 1 || topk_group > n_group || (group_top != 1 && group_top != 2) ||
+      (n_group > 1 && group_top > E / n_group) || k > topk_group * (E / n_group))
+    return GSG_ERR_INVALID_ARG;
+  if (T == 0) return GSG_OK;
+  if (!logits || !topk_ids || !gates) return GSG_ERR_INVALID_ARG;
+  DeviceState* d = nullptr;
+  gsg_status_t st = device_state(&d);
+  if (st != GSG_OK) return st;
+  return from_cuda(gsg::launch_gate(logits, logits_dtype == GSG_OUT_F32, bias, T, E, k, scoring == GSG_SCORE_SIGMOID,
+                                    n_group, topk_group, group_top, renormalize != 0, scale, topk_ids, gates,
+                                    d->status, as_stream(stream)));
+}
+
+gsg_status_t gsg_add_rmsnorm_mx(const uint16_t* x, const void* residual, int residual_dtype, const void* weight,
+                                int weight_dtype, int T, int K, float eps, void* h, uint16_t* y, int fmt,
+                                uint8_t* codes, uint8_t* scales, void* stream) {
+  if (T < 0 || (residual_dtype != GSG_OUT_BF16 && residual_dtype != GSG_OUT_F32) ||
+      (weight_dtype != GSG_OUT_BF16 && weight_dtype != GSG_OUT_F32) || (fmt != 0 && fmt != GSG_MXFP4 && fmt != GSG_MXFP8) ||
+      !(eps >= 0.0f))
+    return GSG_ERR_INVALID_ARG;
+  if (K < 8 || K % 8 != 0 || K > 32768 || (fmt != 0 && K % 256 != 0)) return GSG_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return GSG_OK;
+  if (!x || !weight || (residual != nullptr && !h) || (fmt != 0 && (!codes || !scales)) || (fmt == 0 && !y && !residual))
+    return GSG_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, residual, weight, h, y, codes, scales};
+  for (const void* q : ptrs)
+    if (q != nullptr && !aligned16(q)) return GSG_ERR_INVALID_ARG;
+  DeviceState* d = nullptr;
+  gsg_status_t st = device_state(&d);
+  if (st != GSG_OK) return st;
+  return from_cuda(gsg::launch_add_rmsnorm(x, residual, residual_dtype == GSG_OUT_F32, weight,
+                                           weight_dtype == GSG_OUT_F32, T, K, eps, h, y, fmt, codes, scales, d->status,
+                                           as_stream(stream)));
+}
+
 gsg_status_t gsg_grouped_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int act_fmt, const uint8_t* w_packed,
                                  const int32_t* expert_offsets, int E, int N, int K, int R, int max_rows_per_expert,
                                  void* Y, int y_dtype, void* stream) {

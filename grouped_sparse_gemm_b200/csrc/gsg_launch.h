@@ -42,6 +42,16 @@ cudaError_t launch_pack_mxfp4_codes(const uint8_t* codes, const uint8_t* scales,
 cudaError_t launch_quant_mx(const uint16_t* X, int T, int K, int bits, const int32_t* inv_perm, int k, uint8_t* codes,
                             uint8_t* scales, uint32_t* raw, int* status, int num_sms, cudaStream_t stream);
 
+// gsg_gate.cu
+cudaError_t launch_gate(const void* logits, bool f32, const float* bias, int T, int E, int k, bool sigmoid, int n_group,
+                        int topk_group, int group_top, bool renorm, float scale, int32_t* ids, float* gates,
+                        int* status, cudaStream_t stream);
+
+// gsg_norm.cu (r nullptr: no residual; bits 0: no microscaled output)
+cudaError_t launch_add_rmsnorm(const uint16_t* x, const void* r, int r_f32, const void* w, int w_f32, int T, int K,
+                               float eps, void* h, uint16_t* y, int bits, uint8_t* codes, uint8_t* scales, int* status,
+                               cudaStream_t stream);
+
 // gsg_route.cu
 int route_chunks(int R, int E);
 size_t route_workspace_bytes(int R, int E);

@@ -78,6 +78,9 @@ enum {
 /* Output element types of the grouped GEMMs (and the element types of the calls that take either). */
 enum { GSG_OUT_BF16 = 0, GSG_OUT_F32 = 1 };
 
+/* Router scores of gsg_moe_gate. */
+enum { GSG_SCORE_SOFTMAX = 0, GSG_SCORE_SIGMOID = 1 };
+
 /* Microscaled element formats: E2M1 or E4M3 codes with one UE8M0 scale per 32 values. */
 enum { GSG_MXFP4 = 4, GSG_MXFP8 = 8 };
 
@@ -110,6 +113,27 @@ gsg_status_t gsg_pack_sparse_nvfp4(const float* W, int E, int N, int K, uint8_t*
 gsg_status_t gsg_pack_dense_nvfp4(const float* W, int E, int N, int K, uint8_t* w_packed,
                                   float* w_tensor_scale,
                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* ----------------------------------------------------------------------------------------
+ * gsg_moe_gate -- the router in front of the routing calls: logits to expert ids and gates.  The paper
+ * has no counterpart (it takes ids and gates as given).
+ * logits [T][E] bf16 or fp32 (logits_dtype GSG_OUT_BF16, GSG_OUT_F32), bias fp32 [E] or NULL.
+ *     score s = softmax over the E logits (GSG_SCORE_SOFTMAX) or 1 / (1 + exp(-x)) (GSG_SCORE_SIGMOID)
+ *     choice c = s + bias, in 64-bit arithmetic (fp32 comparisons closer than their error are settled in
+ *                64 bits); without a bias and with group_top 1 the order of the logits themselves
+ * An expert whose logit or bias is -inf is unavailable: c = -inf.
+ * n_group > 1: the experts form n_group groups of E/n_group consecutive ones, a group's score is the sum
+ * of its group_top (1 or 2) largest c, and the experts outside the topk_group best groups are unavailable.
+ * topk_ids int32 [T][k]: the k experts of largest c, descending; gates fp32 [T][k]: their s, 0 for
+ * unavailable ones, divided by the sum of the token's k when renormalize != 0 (all 0 when that is 0), times
+ * `scale`.  Ties go to the lowest index, of groups and of experts.  A token with fewer than k available
+ * experts gets the lowest-numbered others with gate 0, so its ids are distinct and in range.
+ * E <= 1024, k <= 32, n_group <= 32, else GSG_ERR_UNSUPPORTED_SHAPE; E % n_group == 0, k <= topk_group *
+ * E/n_group.  A NaN or +inf logit or bias sets GSG_ERR_NONFINITE (the ids stay in range).  No workspace.
+ */
+gsg_status_t gsg_moe_gate(const void* logits, int logits_dtype, const float* bias, int T, int E, int k, int scoring,
+                          int n_group, int topk_group, int group_top, int renormalize, float scale,
+                          int32_t* topk_ids, float* gates, void* stream);
 
 /* ----------------------------------------------------------------------------------------
  * gsg_moe_route_permute -- group routed rows by expert.
@@ -303,6 +327,20 @@ gsg_status_t gsg_pack_mxfp4_codes(const uint8_t* codes, const uint8_t* scales, i
 gsg_status_t gsg_quantize_act_mx(const uint16_t* X, int T, int K, int fmt, const int32_t* inv_perm, int k,
                                  uint8_t* codes, uint8_t* scales, void* workspace, size_t workspace_bytes,
                                  void* stream);
+
+/* gsg_add_rmsnorm_mx -- residual addition, RMS norm and quantization in one pass.
+ *     h = x + residual, rounded to the residual's type        (residual NULL: h = x, nothing is stored in h)
+ *     y = h * weight / sqrt(mean over K of h^2 + eps)
+ * x bf16 [T][K]; residual and h [T][K] in residual_dtype (GSG_OUT_BF16 or GSG_OUT_F32; h may be the
+ * residual's own buffer); weight [K] in weight_dtype.  y bf16 [T][K], or NULL when it is not wanted.
+ * fmt GSG_MXFP4 or GSG_MXFP8: codes and scales of the unrounded y, rows in token order, as
+ * gsg_grouped_mx_gemm takes them; 0: none (codes, scales unused).  The mean square is summed in more than
+ * 32 bits.  K % 8 == 0 (% 256 with codes), K <= 32768, else GSG_ERR_UNSUPPORTED_SHAPE; eps >= 0 (a row of
+ * zeros with eps 0 has no norm: GSG_ERR_NONFINITE, like every non-finite row).  All pointers 16-byte
+ * aligned.  No workspace. */
+gsg_status_t gsg_add_rmsnorm_mx(const uint16_t* x, const void* residual, int residual_dtype, const void* weight,
+                                int weight_dtype, int T, int K, float eps, void* h, uint16_t* y, int fmt,
+                                uint8_t* codes, uint8_t* scales, void* stream);
 
 /* gsg_grouped_mx_gemm -- for each expert e and routed row r in [off[e], off[e+1]):
  *     Y[r][n] = sum_k a[r][k] * w[e][n][k]      (fp32 accumulation)

@@ -20,6 +20,6 @@ closed forms for the GEMM, the 2.75 bit/weight count, routing invariants and a
 hand-worked golden example under tests/golden/.  Nothing here is "parity
 unpinned".
 """
-from . import codecs, pack, quant, route, gemm, unpermute, layout, swiglu  # noqa: F401
+from . import codecs, pack, quant, route, gemm, unpermute, layout, swiglu, mx, gate  # noqa: F401
 
-__all__ = ["codecs", "pack", "quant", "route", "gemm", "unpermute", "layout", "swiglu"]
+__all__ = ["codecs", "pack", "quant", "route", "gemm", "unpermute", "layout", "swiglu", "mx", "gate"]
