@@ -292,7 +292,7 @@ gsg_status_t gsg_moe_gate(const void* logits, int logits_dtype, const float* bia
   if (st != GSG_OK) return st;
   return from_cuda(gsg::launch_gate(logits, logits_dtype == GSG_OUT_F32, bias, T, E, k, scoring == GSG_SCORE_SIGMOID,
                                     n_group, topk_group, group_top, renormalize != 0, scale, topk_ids, gates,
-                                    d->status, as_stream(stream)));
+                                    d->status, d->num_sms, as_stream(stream)));
 }
 
 gsg_status_t gsg_add_rmsnorm_mx(const uint16_t* x, const void* residual, int residual_dtype, const void* weight,

@@ -21,7 +21,7 @@ struct GateParams {
   const void* logits;   // [T][E]
   const float* bias;    // [E] or nullptr
   int T, E, k;
-  int sigmoid;          // scoring
+  int sigmoid;          // scoring: 1 sigmoid, 0 softmax
   int by_score;         // the choice needs scores (a bias, or groups by the sum of two)
   int n_group, topk_group, group_top, group_size;
   uint32_t group_magic; // e / group_size = e * magic >> 20 for e < 1024
@@ -33,6 +33,8 @@ struct GateParams {
 };
 
 constexpr int kGateWarps = 4;
+// blocks per SM (registers: 64, 128 and 168 a thread)
+constexpr int gate_blocks(int nv) { return nv <= 12 ? 8 : nv <= 16 ? 4 : 3; }
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
 // Order-preserving unsigned key of a float (no NaN); -0 counts as +0.  Every key is above 0.
@@ -78,13 +80,14 @@ __device__ __forceinline__ float bias_of(const GateParams& p, int e) {
   return p.bias != nullptr ? __ldg(p.bias + e) : 0.0f;
 }
 
-// Choice of one expert in 32 bits; softmax: mx the row's largest logit, inv_sum its denominator.
-__device__ __forceinline__ float choice32(const GateParams& p, float mx, float inv_sum, float x, float b) {
-  if (x == neg_inf() || b == neg_inf()) return neg_inf();
-  if (!p.by_score) return x;
-  const float s = p.sigmoid ? __fdividef(1.0f, __fadd_rn(1.0f, __expf(-x)))
-                            : __fmul_rn(__expf(__fsub_rn(x, mx)), inv_sum);
-  return __fadd_rn(s, b);
+// Scores in 32 bits; softmax: mx the row's largest logit, inv_sum 1 / its denominator.
+__device__ __forceinline__ float score_sigmoid(float x) { return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-x))); }
+__device__ __forceinline__ float score_softmax(float x, float mx, float inv_sum) {
+  return __fmul_rn(__expf(__fsub_rn(x, mx)), inv_sum);
+}
+// Is expert e in one of the kept groups?
+__device__ __forceinline__ bool group_open(const GateParams& p, uint32_t kept, int e) {
+  return (kept >> (((uint32_t)e * p.group_magic) >> 20)) & 1u;
 }
 
 // Choice of expert e: from the warp's shared row, or evaluated in 64 bits from the logits.
@@ -97,12 +100,16 @@ struct ExactChoice {
   const GateParams& p;
   size_t row;
   double mx, inv_sum;   // softmax: the row's largest logit and 1 / its denominator
-  __device__ __forceinline__ float logit(int e) const {   // NaN or +inf: unavailable
+  __device__ __forceinline__ float raw_logit(int e) const {    // NaN and +inf: unavailable
     const float x = load_logit<T>(p.logits, row + e);
-    return x < INFINITY && bias_of(p, e) < INFINITY ? x : neg_inf();
+    return x < INFINITY ? x : neg_inf();
+  }
+  __device__ __forceinline__ float clean_bias(int e) const {
+    const float b = bias_of(p, e);
+    return b < INFINITY ? b : neg_inf();
   }
   __device__ __forceinline__ double operator()(int e) const {
-    const double x = (double)logit(e), b = (double)bias_of(p, e);
+    const double x = (double)raw_logit(e), b = (double)clean_bias(e);
     const double q = exp(p.sigmoid ? -x : x - mx);
     const double c = (p.sigmoid ? 1.0 / (1.0 + q) : q * inv_sum) + b;
     return x > -INFINITY && b > -INFINITY ? c : -INFINITY;
@@ -116,7 +123,10 @@ __device__ __forceinline__ V group_score(const GateParams& p, int lane, int lpg,
   V a = -INFINITY, b = -INFINITY;   // the two largest
   if (g < p.n_group)
     for (int j = sub; j < p.group_size; j += lpg) {
-      const V v = value(g * p.group_size + j);
+      // (each group starts lpg further on than the one before: other banks where the size is a multiple of 32)
+      int at = j + g * lpg % p.group_size;
+      at = at < p.group_size ? at : at - p.group_size;
+      const V v = value(g * p.group_size + at);
       b = v > a ? a : (v > b ? v : b);
       a = v > a ? v : a;
     }
@@ -154,193 +164,295 @@ __device__ __forceinline__ uint32_t keep_groups(const GateParams& p, int lane, i
   return bits;
 }
 
+// The order in 64 bits of the choices that lanes < n hold one each: this lane's rank.
+__device__ __forceinline__ int exact_rank(double v, int e, int n) {
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const double o = __shfl_sync(0xffffffffu, v, j);
+    const int oe = __shfl_sync(0xffffffffu, e, j);
+    rank += (o > v || (o == v && oe < e)) ? 1 : 0;
+  }
+  return rank;
+}
+
+// Two fp32 choices this far apart are in their true order.  Twice the error of one: a sigmoid from the fast
+// exponential (2 + 1.16 |x| units, times s (1 - s)) and quotient (2 units) is within 2^-21.3; a softmax score
+// within 2^-18.4 of itself (a denominator of 1024 terms, at most 37 additions in a row) and at most 1 / the
+// denominator; the sum with the bias within half a unit of c.
+__device__ __forceinline__ float order_margin(float tol, float c) { return __fmaf_rn(fabsf(c), 0x1p-22f, tol); }
+
 template <typename T, int NV>
-__global__ void __launch_bounds__(32 * kGateWarps)
+__global__ void __launch_bounds__(32 * kGateWarps, gate_blocks(NV))
 moe_gate_kernel(const GateParams p) {
   extern __shared__ float gate_sh[];   // with groups: the choices of each warp's token, [kGateWarps][E]
+  __shared__ int cand_sh[kGateWarps][32];
+  __shared__ float2 rank_sh[kGateWarps][32];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * kGateWarps + warp;
-  if (t >= p.T) return;
-  float x[NV];
+  const uint32_t below = (1u << lane) - 1u;
+  const int lpg = p.n_group > 16 ? 1 : p.n_group > 8 ? 2 : p.n_group > 4 ? 4 : p.n_group > 2 ? 8 : 16;
+  float* sh = gate_sh + (size_t)warp * p.E;
+  float b[NV];   // the biases; -inf: no such expert, or never available
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = 32 * i + lane;
-    x[i] = e < p.E ? load_logit<T>(p.logits, (size_t)t * p.E + e) : neg_inf();
+    b[i] = e < p.E ? bias_of(p, e) : neg_inf();
+    if (!(b[i] < INFINITY)) { bad = true; b[i] = neg_inf(); }
   }
-  float mx = neg_inf();
+  for (int t = blockIdx.x * kGateWarps + warp; t < p.T; t += gridDim.x * kGateWarps) {
+    const size_t row = (size_t)t * p.E;
+    float c[NV];   // the logits, then the choices
+    float probe = 0.0f, mx = neg_inf();
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = 32 * i + lane;
-    const float b = e < p.E ? bias_of(p, e) : 0.0f;
-    // NaN or +inf: an error; the expert counts as unavailable
-    if (!(x[i] < INFINITY) || !(b < INFINITY)) { bad = true; x[i] = neg_inf(); }
-    mx = fmaxf(mx, x[i]);
-  }
-  if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, GSG_ERR_NONFINITE);
-  mx = warp_max(mx);
-  // softmax denominator, where the scores (not only the chosen experts' ratios) are needed
-  float inv_sum = 0.0f;
-  if (!p.sigmoid && (p.by_score || !p.renorm) && mx > neg_inf()) {
-    float s = 0.0f;
+    for (int i = 0; i < NV; ++i) c[i] = 32 * i + lane < p.E ? load_logit<T>(p.logits, row + 32 * i + lane) : neg_inf();
 #pragma unroll
-    for (int i = 0; i < NV; ++i) s = __fadd_rn(s, __expf(__fsub_rn(x[i], mx)));
-    inv_sum = __frcp_rn(warp_sum(s));
-  }
-  // choices as keys; 0 = no such expert, or taken
-  uint32_t key[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = 32 * i + lane;
-    key[i] = e < p.E ? order_key(choice32(p, mx, inv_sum, x[i], bias_of(p, e))) : 0u;
-  }
-  // how far apart two fp32 choices have to be for their order to be certain: twice the error of a
-  // score (at most 1, its exponential and quotient good to 2^-21; a softmax denominator of E terms to
-  // 2^-18) and of the sum with the bias
-  const float tol1 = p.sigmoid ? 0x1p-19f : 0x1p-17f;
-  bool close = false;
-  uint32_t kept = 0xFFFFFFFFu;
-  const int lpg = p.n_group > 16 ? 1 : p.n_group > 8 ? 2 : p.n_group > 4 ? 4 : p.n_group > 2 ? 8 : 16;
-  float* sh = gate_sh + (size_t)warp * p.E;
-  if (p.n_group > 1) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (32 * i + lane < p.E) sh[32 * i + lane] = key_value(key[i]);
-    __syncwarp();
-    const float score = group_score<float>(p, lane, lpg, SharedChoice{sh});
-    kept = keep_groups<float>(p, lane, lpg, score, p.by_score ? __fmaf_rn(fabsf(score), 0x1p-20f, 2.0f * tol1) : -1.0f, &close);
-    if (!p.by_score) close = false;
-    if (!close) {
+    for (int i = 0; i < NV; ++i) {
+      if (32 * i + lane < p.E) probe = __fmaf_rn(c[i], 0.0f, probe);
+      mx = fmaxf(mx, c[i]);
+    }
+    // bit i: expert 32 i + lane is unavailable by its logit (NaN and +inf are errors)
+    uint32_t closed = 0u;
+    if (__any_sync(0xffffffffu, probe != 0.0f)) {
+      mx = neg_inf();
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const uint32_t e = 32 * i + lane;
-        if (key[i] != 0u && !((kept >> ((e * p.group_magic) >> 20)) & 1u)) key[i] = order_key(neg_inf());
+        if (!(c[i] < INFINITY)) { bad = true; c[i] = neg_inf(); }
+        if (c[i] == neg_inf()) closed |= 1u << i;
+        mx = fmaxf(mx, c[i]);
       }
     }
-  }
-  // k rounds of the largest choice
-  int my_id = 0;
-  float my_x = neg_inf();     // the logit of the expert that this lane (j < k) reports; -inf: unavailable
-  if (!close) {
-    uint32_t taken = 0u;      // bit i: this lane's register i
-    for (int j = 0; j < p.k; ++j) {
-      uint32_t m = 0u;
-      int mi = 0;
-      float mxv = 0.0f;
+    float inv_sum = 0.0f;
+    if (!p.sigmoid) {
+      mx = warp_max(mx);
+      // the denominator, where the scores (not only the chosen experts' ratios) are needed
+      if ((p.by_score || !p.renorm) && mx > neg_inf()) {
+        float s = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const uint32_t ki = (taken >> i) & 1u ? 0u : key[i];
-        if (ki > m) { m = ki; mi = i; mxv = x[i]; }
+        for (int i = 0; i < NV; ++i) s = __fadd_rn(s, __expf(__fsub_rn(c[i], mx)));
+        inv_sum = __frcp_rn(warp_sum(s));
       }
-      const uint32_t best = __reduce_max_sync(0xffffffffu, m);
-      const uint32_t e = __reduce_min_sync(0xffffffffu, m == best ? (uint32_t)(32 * mi + lane) : 0xFFFFFFFFu);
-      const float c = key_value(best);
-      const float xw = __shfl_sync(0xffffffffu, mxv, (int)(e & 31u));
-      if ((e & 31u) == (uint32_t)lane) taken |= 1u << (e >> 5);
-      if (lane == j) { my_id = (int)e; my_x = c == neg_inf() ? c : xw; }
-      if (p.by_score && c > neg_inf()) {
-        // another expert within the error bound, other than by the same logit and bias
-        const float lim = __fsub_rn(c, __fmaf_rn(fabsf(c), 0x1p-21f, tol1));
-        bool near = false;
+    }
+    const float tol = !p.by_score ? 0.0f : p.sigmoid ? 0x1p-20f : __fmul_rn(inv_sum, 0x1p-17f);
+    if (p.by_score) {
+      if (p.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) c[i] = __fadd_rn(score_sigmoid(c[i]), b[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) c[i] = __fadd_rn(score_softmax(c[i], mx, inv_sum), b[i]);
+      }
+      if (__any_sync(0xffffffffu, closed != 0u)) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if (!((taken >> i) & 1u) && key[i] > order_key(neg_inf()) && key_value(key[i]) >= lim)
-            near |= x[i] != xw || bias_of(p, 32 * i + lane) != bias_of(p, (int)e);
-        if (__any_sync(0xffffffffu, near)) { close = true; break; }
+          if ((closed >> i) & 1u) c[i] = neg_inf();
       }
     }
-  }
-  if (close) {
-    // the same in 64 bits: rare, so the logits are read again and the choices evaluated where they are
-    // compared, which keeps this path's registers out of the usual one's
-    ExactChoice<T> choice = {p, (size_t)t * p.E, (double)mx, 0.0};
-    if (!p.sigmoid) {
+    ExactChoice<T> exact = {p, row, (double)mx, 0.0};
+    bool have_exact_sum = false;
+    auto exact_sum = [&]() {   // the softmax denominator in 64 bits
+      if (p.sigmoid || have_exact_sum) return;
       double s = 0.0;
 #pragma unroll 1
-      for (int e = lane; e < p.E; e += 32) s += exp((double)choice.logit(e) - choice.mx);
-      choice.inv_sum = 1.0 / warp_sum(s);
-    }
-    kept = 0xFFFFFFFFu;
+      for (int e = lane; e < p.E; e += 32) s += exp((double)exact.raw_logit(e) - exact.mx);
+      exact.inv_sum = 1.0 / warp_sum(s);
+      have_exact_sum = true;
+    };
+    uint32_t kept = 0xFFFFFFFFu;   // groups
     if (p.n_group > 1) {
-      const double score = group_score<double>(p, lane, lpg, choice);
-      bool unused;
-      kept = keep_groups<double>(p, lane, lpg, score, -1.0, &unused);
-    }
-    uint32_t taken = 0u;
-#pragma unroll 1
-    for (int j = 0; j < p.k; ++j) {
-      unsigned long long m = 0ull;
-      int me = 0;
-#pragma unroll 1
-      for (int e = lane; e < p.E; e += 32) {
-        if ((taken >> (e >> 5)) & 1u) continue;
-        const bool open = p.n_group <= 1 || ((kept >> (((uint32_t)e * p.group_magic) >> 20)) & 1u);
-        const unsigned long long ke = order_key(open ? choice(e) : -INFINITY);
-        if (ke > m) { m = ke; me = e; }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (32 * i + lane < p.E) sh[32 * i + lane] = c[i];
+      __syncwarp();
+      const float score = group_score<float>(p, lane, lpg, SharedChoice{sh});
+      bool close = false;
+      kept = keep_groups<float>(p, lane, lpg, score,
+                                p.by_score ? __fmaf_rn(fabsf(score), 0x1p-20f, 2.0f * tol) : -1.0f, &close);
+      if (close && p.by_score) {
+        exact_sum();
+        const double score64 = group_score<double>(p, lane, lpg, exact);
+        kept = keep_groups<double>(p, lane, lpg, score64, -1.0, &close);
       }
-      const unsigned long long best = warp_max_u64(m);
-      const uint32_t e = __reduce_min_sync(0xffffffffu, m == best ? (uint32_t)me : 0xFFFFFFFFu);
-      if ((e & 31u) == (uint32_t)lane) taken |= 1u << (e >> 5);
-      if (lane == j) {
-        my_id = (int)e;
-        my_x = best == order_key(-(double)INFINITY) ? neg_inf() : choice.logit((int)e);
-      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (!group_open(p, kept, 32 * i + lane)) c[i] = neg_inf();
     }
-  }
-  // gates of the chosen experts.  Renormalised ones are ratios of scores, so a common factor may go:
-  // exp(x - max of the chosen) for softmax; for the sigmoid exp(x - m) / (1 + exp(x)), m = min(0, that max),
-  // which keeps scores that would underflow apart.
-  const float mc = warp_max(lane < p.k ? my_x : neg_inf());
-  float g = 0.0f;
-  if (lane < p.k && my_x > neg_inf()) {
-    if (p.sigmoid) {
-      const float m = p.renorm ? fminf(mc, 0.0f) : 0.0f;
-      g = my_x > 0.0f ? __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-my_x)))
-                      : __fdiv_rn(expf(__fsub_rn(my_x, m)), __fadd_rn(1.0f, expf(my_x)));
+    // At least k experts have the k-th largest of the 32 lanes' maxima or more; the chosen ones, and all
+    // whose order with them is uncertain, are among those that come up to it less the margin.
+    float m = c[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) m = fmaxf(m, c[i]);
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+      for (int stride = size / 2; stride > 0; stride /= 2) {   // bitonic sort, descending
+        const float o = __shfl_xor_sync(0xffffffffu, m, stride);
+        m = ((lane & size) == 0) == ((lane & stride) == 0) ? fmaxf(m, o) : fminf(m, o);
+      }
+    const float kth = __shfl_sync(0xffffffffu, m, p.k - 1);
+    const float lim = p.by_score ? __fsub_rn(kth, order_margin(tol, kth)) : kth;
+    uint32_t mask = 0u;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) mask |= c[i] >= lim && 32 * i + lane < p.E ? 1u << i : 0u;
+    const int n = __reduce_add_sync(0xffffffffu, __popc(mask));
+    int my_e = 0, rank = 32;      // this lane's chosen expert and its place among the k (>= k: none)
+    float my_x = neg_inf();       // its logit; -inf: unavailable
+    if (n <= 32) {
+      // one candidate per lane
+      int base = 0;
+      for (uint32_t live; (live = __ballot_sync(0xffffffffu, mask != 0u)) != 0u; base += __popc(live))
+        if (mask != 0u) {
+          cand_sh[warp][base + __popc(live & below)] = 32 * (__ffs(mask) - 1) + lane;
+          mask &= mask - 1u;
+        }
+      __syncwarp();
+      float v = neg_inf();
+      if (lane < n) {
+        my_e = cand_sh[warp][lane];
+        const float be = exact.clean_bias(my_e);
+        my_x = exact.raw_logit(my_e);
+        if (be == neg_inf() || !group_open(p, kept, my_e)) my_x = neg_inf();
+        if (my_x > neg_inf())
+          v = !p.by_score ? my_x : __fadd_rn(p.sigmoid ? score_sigmoid(my_x) : score_softmax(my_x, mx, inv_sum), be);
+      }
+      rank_sh[warp][lane] = make_float2(v, __int_as_float(my_e));
+      __syncwarp();
+      const float margin = order_margin(tol, v);
+      bool near = false;
+      rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const float2 o = rank_sh[warp][j];
+        const int oe = __float_as_int(o.y);
+        rank += (o.x > v || (o.x == v && oe < my_e)) ? 1 : 0;
+        near |= fabsf(__fsub_rn(o.x, v)) <= margin && oe != my_e;
+      }
+      if (p.by_score && __any_sync(0xffffffffu, near && lane < n && rank < p.k)) {
+        exact_sum();
+        rank = exact_rank(my_x > neg_inf() ? exact(my_e) : -(double)INFINITY, my_e, n);
+      }
+      if (lane >= n) rank = 32;
+      __syncwarp();   // the candidates are read before the next token's are written
     } else {
-      g = p.renorm ? expf(__fsub_rn(my_x, mc)) : __fmul_rn(expf(__fsub_rn(my_x, mx)), inv_sum);
+      // many near the k-th (k above 16, long ties, unavailable experts): k rounds of the largest choice
+      bool close = false;
+      uint32_t taken = 0u;      // bit i: expert 32 i + lane
+#pragma unroll 1
+      for (int j = 0; j < p.k; ++j) {
+        uint32_t best_key = 0u;
+        int bi = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const uint32_t ki = (taken >> i) & 1u || 32 * i + lane >= p.E ? 0u : order_key(c[i]);
+          if (ki > best_key) { best_key = ki; bi = i; }
+        }
+        const uint32_t best = __reduce_max_sync(0xffffffffu, best_key);
+        const int e = (int)__reduce_min_sync(0xffffffffu, best_key == best ? (uint32_t)(32 * bi + lane) : 0xFFFFFFFFu);
+        const float v = key_value(best);
+        if ((e & 31) == lane) taken |= 1u << (e >> 5);
+        if (lane == j) { my_e = e; rank = j; my_x = v == neg_inf() ? v : exact.raw_logit(e); }
+        if (p.by_score && v > neg_inf()) {
+          // another expert whose order is uncertain, other than by the same logit and bias (an equal score)
+          const float near_lim = __fsub_rn(v, order_margin(tol, v));
+          uint32_t near_mask = 0u;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) near_mask |= c[i] >= near_lim && c[i] > neg_inf() ? 1u << i : 0u;
+          near_mask &= ~taken;
+          const float xe = exact.raw_logit(e), be = exact.clean_bias(e);
+          bool near = false;
+          for (; near_mask != 0u; near_mask &= near_mask - 1u) {
+            const int o = 32 * (__ffs(near_mask) - 1) + lane;
+            near |= exact.raw_logit(o) != xe || exact.clean_bias(o) != be;
+          }
+          close = __any_sync(0xffffffffu, near);
+          if (close) break;
+        }
+      }
+      if (close) {   // the same in 64 bits; choices evaluated where they are compared
+        exact_sum();
+        taken = 0u;
+#pragma unroll 1
+        for (int j = 0; j < p.k; ++j) {
+          unsigned long long best_key = 0ull;
+          int best_e = 0;
+#pragma unroll 1
+          for (int e = lane; e < p.E; e += 32) {
+            if ((taken >> (e >> 5)) & 1u) continue;
+            const unsigned long long ke = order_key(group_open(p, kept, e) ? exact(e) : -(double)INFINITY);
+            if (ke > best_key) { best_key = ke; best_e = e; }
+          }
+          const unsigned long long best = warp_max_u64(best_key);
+          const int e = (int)__reduce_min_sync(0xffffffffu, best_key == best ? (uint32_t)best_e : 0xFFFFFFFFu);
+          if ((e & 31) == lane) taken |= 1u << (e >> 5);
+          if (lane == j) {
+            my_e = e;
+            rank = j;
+            my_x = best == order_key(-(double)INFINITY) ? neg_inf() : exact.raw_logit(e);
+          }
+        }
+      }
+    }
+    // gates of the chosen experts.  Renormalised ones are ratios of scores, so a common factor may go:
+    // exp(x - max of the chosen) for softmax; for the sigmoid exp(x - m) / (1 + exp(x)), m = min(0, that max),
+    // which keeps scores that would underflow apart.
+    const bool chosen = rank < p.k;
+    const float mc = warp_max(chosen ? my_x : neg_inf());
+    float g = 0.0f;
+    if (chosen && my_x > neg_inf()) {
+      if (p.sigmoid) {
+        const float off = p.renorm ? fminf(mc, 0.0f) : 0.0f;
+        g = my_x > 0.0f ? __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-my_x)))
+                        : __fdiv_rn(expf(__fsub_rn(my_x, off)), __fadd_rn(1.0f, expf(my_x)));
+      } else {
+        g = p.renorm ? expf(__fsub_rn(my_x, mc)) : __fmul_rn(expf(__fsub_rn(my_x, mx)), inv_sum);
+      }
+    }
+    if (p.renorm) {
+      const float sum = warp_sum(g);
+      g = sum > 0.0f ? __fdiv_rn(g, sum) : 0.0f;
+    }
+    if (chosen) {
+      p.ids[(size_t)t * p.k + rank] = my_e;
+      p.gates[(size_t)t * p.k + rank] = __fmul_rn(g, p.scale);
     }
   }
-  if (p.renorm) {
-    const float sum = warp_sum(g);
-    g = sum > 0.0f ? __fdiv_rn(g, sum) : 0.0f;
-  }
-  if (lane < p.k) {
-    p.ids[(size_t)t * p.k + lane] = my_id;
-    p.gates[(size_t)t * p.k + lane] = __fmul_rn(g, p.scale);
-  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, GSG_ERR_NONFINITE);
 }
 
 template <typename T, int NV>
-static cudaError_t launch_gate_nv(const GateParams& p, cudaStream_t stream) {
-  const unsigned grid = (unsigned)((p.T + kGateWarps - 1) / kGateWarps);
+static cudaError_t launch_gate_nv(const GateParams& p, int num_sms, cudaStream_t stream) {
+  // a warp keeps the biases and takes token after token; as many blocks as fit the device
+  unsigned grid = (unsigned)((p.T + kGateWarps - 1) / kGateWarps);
+  const unsigned most = (unsigned)num_sms * gate_blocks(NV);
+  if (grid > most) grid = most;
   const size_t sh = p.n_group > 1 ? (size_t)kGateWarps * p.E * sizeof(float) : 0;
   return launch_pdl(moe_gate_kernel<T, NV>, grid, 32 * kGateWarps, sh, stream, p);
 }
 
 template <typename T>
-static cudaError_t launch_gate_t(const GateParams& p, cudaStream_t stream) {
+static cudaError_t launch_gate_t(const GateParams& p, int num_sms, cudaStream_t stream) {
   const int nv = (p.E + 31) / 32;
-  if (nv <= 2) return launch_gate_nv<T, 2>(p, stream);
-  if (nv <= 4) return launch_gate_nv<T, 4>(p, stream);
-  if (nv <= 8) return launch_gate_nv<T, 8>(p, stream);
-  if (nv <= 12) return launch_gate_nv<T, 12>(p, stream);
-  if (nv <= 16) return launch_gate_nv<T, 16>(p, stream);
-  return launch_gate_nv<T, 32>(p, stream);
+  if (nv <= 1) return launch_gate_nv<T, 1>(p, num_sms, stream);
+  if (nv <= 2) return launch_gate_nv<T, 2>(p, num_sms, stream);
+  if (nv <= 4) return launch_gate_nv<T, 4>(p, num_sms, stream);
+  if (nv <= 8) return launch_gate_nv<T, 8>(p, num_sms, stream);
+  if (nv <= 12) return launch_gate_nv<T, 12>(p, num_sms, stream);
+  if (nv <= 16) return launch_gate_nv<T, 16>(p, num_sms, stream);
+  return launch_gate_nv<T, 32>(p, num_sms, stream);
 }
 
 cudaError_t launch_gate(const void* logits, bool f32, const float* bias, int T, int E, int k, bool sigmoid, int n_group,
                         int topk_group, int group_top, bool renorm, float scale, int32_t* ids, float* gates,
-                        int* status, cudaStream_t stream) {
+                        int* status, int num_sms, cudaStream_t stream) {
   GateParams p;
   p.logits = logits; p.bias = bias; p.T = T; p.E = E; p.k = k;
   p.sigmoid = sigmoid; p.by_score = bias != nullptr || (n_group > 1 && group_top == 2);
   p.n_group = n_group; p.topk_group = topk_group; p.group_top = group_top; p.group_size = E / n_group;
   p.group_magic = (uint32_t)(((1u << 20) + p.group_size - 1) / p.group_size);
   p.renorm = renorm; p.scale = scale; p.ids = ids; p.gates = gates; p.status = status;
-  return f32 ? launch_gate_t<float>(p, stream) : launch_gate_t<uint16_t>(p, stream);
+  return f32 ? launch_gate_t<float>(p, num_sms, stream) : launch_gate_t<uint16_t>(p, num_sms, stream);
 }
 
 }  // namespace gsg

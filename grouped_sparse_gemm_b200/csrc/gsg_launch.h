@@ -45,7 +45,7 @@ cudaError_t launch_quant_mx(const uint16_t* X, int T, int K, int bits, const int
 // gsg_gate.cu
 cudaError_t launch_gate(const void* logits, bool f32, const float* bias, int T, int E, int k, bool sigmoid, int n_group,
                         int topk_group, int group_top, bool renorm, float scale, int32_t* ids, float* gates,
-                        int* status, cudaStream_t stream);
+                        int* status, int num_sms, cudaStream_t stream);
 
 // gsg_norm.cu (r nullptr: no residual; bits 0: no microscaled output)
 cudaError_t launch_add_rmsnorm(const uint16_t* x, const void* r, int r_f32, const void* w, int w_f32, int T, int K,

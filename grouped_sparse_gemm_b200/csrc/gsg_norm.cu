@@ -4,11 +4,12 @@
 //   y = h * w / sqrt(v);   outputs: h, y in bf16, y in MXFP8 or MXFP4 (from the unrounded y)
 //
 // A block holds one row in registers, so every input is read once and every output written once.
-// The squares are summed in fp32 over eight values and in 64 bits beyond, and 1 / sqrt(v) is the fp32
-// estimate after one Newton step in 64 bits, applied as a sum of two fp32 numbers.  y is rounded to fp32
-// "to odd" (see round_odd), so that its later rounding to a code or to bf16 is the rounding of the value
-// before it, not of a value that has been rounded onto a border between two codes.  (h may be the residual's own buffer: each thread reads its values, through the
-// coherent path, before it stores them.)
+// The squares are summed in 64 bits, and 1 / sqrt(v) is taken in 64 bits and applied as a sum of two fp32
+// numbers (in 64 bits throughout where those leave the fp32 range's middle).  y is rounded to fp32 "to odd"
+// (see round_odd), so that its later rounding to a code or to bf16 is the rounding of the value before it,
+// not of a value that has been rounded onto a border between two codes: with sums of eight squares in fp32,
+// which is 2^-31 off, a few of 58.7 million codes still came out on the wrong side.  (h may be the
+// residual's own buffer: each thread reads its values, through the coherent path, before it stores them.)
 #include "gsg_launch.h"
 #include "gsg_mx.cuh"
 
@@ -57,12 +58,14 @@ __device__ __forceinline__ float round_odd(float v, float rest) {
   return __uint_as_float(u);
 }
 
+constexpr int kNormThreads = 512;
+
 // kRes: 0 no residual, 1 bf16, 2 fp32.  kBits: 0 no microscaled output, 4, 8.  A thread holds kU units
 // of eight consecutive values, unit i * blockDim.x + threadIdx.x of the row; four neighbouring lanes
 // hold a 32-block and sixteen a 128-wide k-block (K % 256 == 0 with microscaled output, so the lanes
 // of a k-block are all in the row or all past its end).
 template <int kRes, int kBits, int kU>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(kNormThreads)
 add_rmsnorm_kernel(const NormParams p) {
   __shared__ double red[32];
   pdl_launch_dependents();
@@ -127,21 +130,19 @@ add_rmsnorm_kernel(const NormParams p) {
   // ---- mean square
   double sum = 0.0;
 #pragma unroll
-  for (int i = 0; i < kU; ++i) {
-    float s = 0.0f;
+  for (int i = 0; i < kU; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s = __fmaf_rn(v[i][j], v[i][j], s);
-    sum += (double)s;
-  }
+    for (int j = 0; j < 8; ++j) sum = __fma_rn((double)v[i][j], (double)v[i][j], sum);
   sum = warp_sum_d(sum);
   if (lane == 0) red[warp] = sum;
   __syncthreads();
   sum = warp_sum_d(lane < nw ? red[lane] : 0.0);
   const double var = sum / (double)p.K + (double)p.eps;
   if (!(var < (double)INFINITY) && threadIdx.x == 0) set_status(p.status, GSG_ERR_NONFINITE);
-  double rd = (double)rsqrtf((float)var);
-  rd = rd * (1.5 - 0.5 * var * rd * rd);
+  const double rd = rsqrt(var);
   const float rh = (float)rd, rl = (float)(rd - (double)rh);
+  // products of h, w and rh stay clear of the fp32 range's ends (for weights below 2^60)
+  const bool middle = rh > 0x1p-60f && rh < 0x1p60f;
   // ---- scaled row
 #pragma unroll
   for (int i = 0; i < kU; ++i) {
@@ -164,6 +165,16 @@ add_rmsnorm_kernel(const NormParams p) {
       const float c = __fmaf_rn(q, rl, __fmul_rn(qe, rh));
       const float s = __fmaf_rn(q, rh, c);
       y[j] = round_odd(s, __fadd_rn(__fmaf_rn(q, rh, -s), c));
+    }
+    if (!middle) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float h = v[i][j];
+        asm volatile("" : "+f"(h));   // not the sum's conversion kept in a register pair until here
+        const double d = (double)h * (double)w[j] * rd;
+        const float s = (float)d;
+        y[j] = round_odd(s, (float)(d - (double)s));
+      }
     }
     if (p.y != nullptr && in)
       reinterpret_cast<uint4*>(p.y + row)[u] =
@@ -203,12 +214,13 @@ add_rmsnorm_kernel(const NormParams p) {
 template <int kRes, int kBits>
 static cudaError_t launch_norm_u(const NormParams& p, cudaStream_t stream) {
   const int upr = p.K / 8;
-  // units per thread: enough threads to hide the loads of one row, at most 1024
-  const int kU = upr <= 512 ? 1 : upr <= 1024 ? 2 : 4;
+  // units per thread: as few as a block of 512 threads allows, to hide the loads of one row
+  const int kU = upr <= kNormThreads ? 1 : upr <= 2 * kNormThreads ? 2 : upr <= 4 * kNormThreads ? 4 : 8;
   const int threads = (((upr + kU - 1) / kU) + 31) / 32 * 32;
   if (kU == 1) return launch_pdl(add_rmsnorm_kernel<kRes, kBits, 1>, p.T, threads, 0, stream, p);
   if (kU == 2) return launch_pdl(add_rmsnorm_kernel<kRes, kBits, 2>, p.T, threads, 0, stream, p);
-  return launch_pdl(add_rmsnorm_kernel<kRes, kBits, 4>, p.T, threads, 0, stream, p);
+  if (kU == 4) return launch_pdl(add_rmsnorm_kernel<kRes, kBits, 4>, p.T, threads, 0, stream, p);
+  return launch_pdl(add_rmsnorm_kernel<kRes, kBits, 8>, p.T, threads, 0, stream, p);
 }
 
 template <int kRes>
