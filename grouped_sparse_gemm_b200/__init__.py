@@ -529,20 +529,21 @@ def _args(stream, *ts: Optional[torch.Tensor]) -> int:
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError("grouped_sparse_gemm_b200 works on CUDA tensors only (no CPU fallback)")
-        if t.get_device() != dev:
-            raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is cuda:{dev}")
-        if not t.is_contiguous():
+        if t.get_device() != dev or not t.is_contiguous():
+            if not t.is_cuda:
+                raise ValueError("grouped_sparse_gemm_b200 works on CUDA tensors only (no CPU fallback)")
+            if t.get_device() != dev:
+                raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is cuda:{dev}")
             raise ValueError("tensors must be contiguous")
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+    # (the raw handle: building a Stream object takes 3 us, as long as the rest of a small call)
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _out(t: Optional[torch.Tensor], shape, dtype, device, what: str) -> torch.Tensor:
-    """A new output, or the caller's after a check of its shape and type."""
+def _out(t: Optional[torch.Tensor], shape, like: torch.Tensor, dtype, what: str) -> torch.Tensor:
+    """A new output on the device of `like`, or the caller's after a check of its shape and type."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        return like.new_empty(shape, dtype=dtype)
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} {dtype}")
     return t
 
@@ -551,24 +552,24 @@ def _ptr_of(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _mx_activations(out: Optional[MxActivations], R: int, K: int, fmt: int, device) -> MxActivations:
-    if fmt not in (MXFP4, MXFP8):
+def _mx_activations(out: Optional[MxActivations], R: int, K: int, fmt: int, like: torch.Tensor) -> MxActivations:
+    if fmt != MXFP4 and fmt != MXFP8:
         raise ValueError(f"fmt {fmt!r}: MXFP4 (4) or MXFP8 (8)")
-    codes, scales = (None, None) if out is None else (out.codes, out.scales)
-    codes = _out(codes, (R, K * fmt // 8), torch.uint8, device, "codes")
-    scales = _out(scales, (K // 128 * R * 16,), torch.uint8, device, "scales")
     if out is None:
-        return MxActivations(codes, scales, R, K, fmt)
+        return MxActivations(like.new_empty((R, K * fmt // 8), dtype=torch.uint8),
+                             like.new_empty((K // 128 * R * 16,), dtype=torch.uint8), R, K, fmt)
     if (out.R, out.K, out.fmt) != (R, K, fmt):
         raise ValueError(f"out: R={out.R} K={out.K} fmt={out.fmt}, expected R={R} K={K} fmt={fmt}")
+    _out(out.codes, (R, K * fmt // 8), like, torch.uint8, "codes")
+    _out(out.scales, (K // 128 * R * 16,), like, torch.uint8, "scales")
     return out
 
 
-def _mx_weights(out: Optional[PackedMxWeights], E: int, N: int, K: int, device) -> PackedMxWeights:
+def _mx_weights(out: Optional[PackedMxWeights], E: int, N: int, K: int, like: torch.Tensor) -> PackedMxWeights:
     n = int(lib().gsg_mx_packed_bytes(E, N, K))
     if out is not None and (out.E, out.N, out.K) != (E, N, K):
         raise ValueError(f"out: E={out.E} N={out.N} K={out.K}, expected E={E} N={N} K={K}")
-    packed = _out(None if out is None else out.packed, (n,), torch.uint8, device, "packed")
+    packed = _out(None if out is None else out.packed, (n,), like, torch.uint8, "packed")
     return out if out is not None else PackedMxWeights(packed, E, N, K)
 
 
@@ -588,8 +589,8 @@ def moe_gate(logits: torch.Tensor, top_k: int, scoring: str = "softmax", bias: O
     if bias is not None and (bias.dtype != torch.float32 or bias.numel() != E):
         raise ValueError(f"bias: fp32 of {E} entries wanted")
     s = _args(stream, logits, bias, out_ids, out_gates)
-    out_ids = _out(out_ids, (T, top_k), torch.int32, logits.device, "out_ids")
-    out_gates = _out(out_gates, (T, top_k), torch.float32, logits.device, "out_gates")
+    out_ids = _out(out_ids, (T, top_k), logits, torch.int32, "out_ids")
+    out_gates = _out(out_gates, (T, top_k), logits, torch.float32, "out_gates")
     _check("gsg_moe_gate", lib().gsg_moe_gate(
         logits.data_ptr(), OUT_F32 if logits.dtype == torch.float32 else OUT_BF16, _ptr_of(bias), T, E, top_k,
         _SCORES[scoring], n_group, topk_group, group_top, 1 if renormalize else 0, scale, out_ids.data_ptr(),
@@ -615,11 +616,11 @@ def add_rmsnorm_mx(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     if residual is not None:
         if residual.shape != x.shape or residual.dtype not in (torch.float32, torch.bfloat16):
             raise ValueError(f"residual: fp32 or bf16 {tuple(x.shape)} wanted")
-        h = _out(out_h, (T, K), residual.dtype, x.device, "out_h")
+        h = _out(out_h, x.shape, x, residual.dtype, "out_h")
     if want_y or out_y is not None:
-        y = _out(out_y, (T, K), torch.bfloat16, x.device, "out_y")
+        y = _out(out_y, x.shape, x, torch.bfloat16, "out_y")
     if fmt is not None:
-        act = _mx_activations(out_act, T, K, fmt, x.device)
+        act = _mx_activations(out_act, T, K, fmt, x)
     _check("gsg_add_rmsnorm_mx", lib().gsg_add_rmsnorm_mx(
         x.data_ptr(), _ptr_of(residual), OUT_F32 if h is not None and h.dtype == torch.float32 else OUT_BF16,
         weight.data_ptr(), OUT_F32 if weight.dtype == torch.float32 else OUT_BF16, T, K, eps, _ptr_of(h), _ptr_of(y),
@@ -634,7 +635,7 @@ def pack_mxfp4(W: torch.Tensor, out: Optional[PackedMxWeights] = None, stream=No
         raise ValueError(f"W: fp32 or bf16 [E, N, K] wanted, got {W.dtype} {tuple(W.shape)}")
     E, N, K = W.shape
     s = _args(stream, W, None if out is None else out.packed)
-    out = _mx_weights(out, E, N, K, W.device)
+    out = _mx_weights(out, E, N, K, W)
     _check("gsg_pack_mxfp4", lib().gsg_pack_mxfp4(
         W.data_ptr(), OUT_F32 if W.dtype == torch.float32 else OUT_BF16, E, N, K, out.packed.data_ptr(), s))
     return out
@@ -650,7 +651,7 @@ def pack_mxfp4_codes(codes: torch.Tensor, scales: torch.Tensor, out: Optional[Pa
     if tuple(scales.shape) != (E, N, K // 32):
         raise ValueError(f"scales: {tuple(scales.shape)}, expected {(E, N, K // 32)}")
     s = _args(stream, codes, scales, None if out is None else out.packed)
-    out = _mx_weights(out, E, N, K, codes.device)
+    out = _mx_weights(out, E, N, K, codes)
     _check("gsg_pack_mxfp4_codes", lib().gsg_pack_mxfp4_codes(
         codes.data_ptr(), scales.data_ptr(), E, N, K, out.packed.data_ptr(), s))
     return out
@@ -666,7 +667,7 @@ def quantize_act_mx(X: torch.Tensor, fmt: int = MXFP8, inv_perm: Optional[torch.
     if inv_perm is not None and (inv_perm.dtype != torch.int32 or inv_perm.numel() < T * top_k):
         raise ValueError(f"inv_perm: int32 of {T * top_k} entries wanted")
     s = _args(stream, X, inv_perm, workspace, None if out is None else out.codes, None if out is None else out.scales)
-    out = _mx_activations(out, T * top_k, K, fmt, X.device)
+    out = _mx_activations(out, T * top_k, K, fmt, X)
     L = lib()
     if workspace is None and T * top_k * K >= 1 << 27:   # (below that the call needs none)
         workspace = _workspace(L.gsg_workspace_size(OP_QUANTIZE_MX, 0, 0, K, T, top_k), X.device)
@@ -690,7 +691,7 @@ def grouped_mx_gemm(act: MxActivations, w: PackedMxWeights, offsets: torch.Tenso
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"out: bf16 or fp32, got {out_dtype}")
     s = _args(stream, act.codes, act.scales, w.packed, offsets, out)
-    out = _out(out, (act.R, w.N), out_dtype, act.codes.device, "out")
+    out = _out(out, (act.R, w.N), act.codes, out_dtype, "out")
     _check("gsg_grouped_mx_gemm", lib().gsg_grouped_mx_gemm(
         act.codes.data_ptr(), act.scales.data_ptr(), act.fmt, w.packed.data_ptr(), offsets.data_ptr(), w.E, w.N, w.K,
         act.R, max_rows_per_expert, out.data_ptr(), OUT_F32 if out_dtype == torch.float32 else OUT_BF16, s))

@@ -37,6 +37,7 @@ gsg_status_t device_state(DeviceState** out) {
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return GSG_ERR_CUDA;
     if (gsg::route_set_smem_attrs() != cudaSuccess) return GSG_ERR_CUDA;
     if (gsg::gemm_set_smem_attrs() != cudaSuccess) return GSG_ERR_CUDA;
+    if (gsg::quant_mx_set_smem_attrs() != cudaSuccess) return GSG_ERR_CUDA;
     d.status = static_cast<int*>(p);
     d.num_sms = sms;
     d.ready = true;

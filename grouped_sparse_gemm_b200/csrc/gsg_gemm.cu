@@ -45,14 +45,12 @@ constexpr int kGemmThreads = 352;
 // a wide pair tile adds four epilogue warps (11..14) that drain the tile's second n-tile while
 // warps 3..6 drain the first
 constexpr int kGemmThreadsWide = 480;
-__host__ __device__ constexpr int gemm_threads(bool wide) { return wide ? kGemmThreadsWide : kGemmThreads; }
+constexpr int kScaleRing = 4;              // microscaled formats: stages of the scale ring
 constexpr int kMaxE = 1024;
 constexpr int kMaxAcc = 8;
 constexpr int kNSets = 3;                  // TMEM sets of metadata + scales
-constexpr uint32_t kSetCols = 64;
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;   // 2 s
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColAcc = kNSets * kSetCols;       // first accumulator (192)
 constexpr int kOutStageBytes = 16 * 32 * 4;           // epilogue transpose buffer per warp
 constexpr int kGluStageBytes = 32 * 36 * 4;           // SwiGLU epilogue: 32 tokens x 32 features (+4 pad)
 
@@ -64,6 +62,12 @@ constexpr int kGluStageBytes = 32 * 36 * 4;           // SwiGLU epilogue: 32 tok
 //    That MMA reads 4-bit operands from 16-byte groups of 16 values (8 bytes of codes, 8 of padding);
 //    the TMA writes that form into shared memory from the packed codes, so HBM and L2 carry 4 bits.
 constexpr int kFmtDense = kGemmDense, kFmtSparse = kGemmSparse, kFmtMx4 = kGemmMx4, kFmtMx8 = kGemmMx8;
+
+__host__ __device__ constexpr bool fmt_mx(int fmt) { return fmt == kFmtMx4 || fmt == kFmtMx8; }
+// (the microscaled formats have a warp more, the scale producer)
+__host__ __device__ constexpr int gemm_threads(int fmt, bool wide) {
+  return (wide ? kGemmThreadsWide : kGemmThreads) + (fmt_mx(fmt) ? 32 : 0);
+}
 
 struct GemmParams {
   const uint8_t* a_scales;
@@ -160,14 +164,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred P;\n\t" GSG_ELECT
-      "@P cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::
-          "r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
 // Per-lane forms: every lane of the (converged) warp executes the instruction and the lanes with
 // `on` set each issue their own copy.  The TMA unit works through the copies of one issuing thread
 // one after another, so the copies of a stage are spread over lanes to be in flight together.
@@ -187,13 +183,15 @@ __device__ __forceinline__ void tma_load_2d_lane(bool on, uint32_t dst, const CU
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"((uint32_t)on)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_3d_lane(bool on, uint32_t dst, const CUtensorMap* map, int x, int y, int z,
-                                                 uint32_t bar) {
+// Pair form: the copy goes to this CTA's own shared memory and completes on a barrier that may be the
+// other CTA's (a shared::cluster address).
+__device__ __forceinline__ void tma_load_2d_lane_pair(bool on, uint32_t dst, const CUtensorMap* map, int x, int y,
+                                                      uint32_t cluster_bar) {
   asm volatile(
-      "{\n\t.reg .pred P;\n\tsetp.ne.b32 P, %6, 0;\n\t"
-      "@P cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::
+      "{\n\t.reg .pred P;\n\tsetp.ne.b32 P, %5, 0;\n\t"
+      "@P cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::
           "r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"((uint32_t)on)
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(cluster_bar), "r"((uint32_t)on)
       : "memory");
 }
 __device__ __forceinline__ void lds128(uint32_t saddr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
@@ -308,8 +306,16 @@ __device__ __forceinline__ void tc_mma_mx(uint32_t d, uint64_t adesc, uint64_t b
   }
 #undef GSG_MX_MMA
 }
+// Two accumulators times `scale` (the microscaled formats have none), rounded to bf16, lo in the low half.
+template <bool kScaled>
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi, float scale) {
+  const __nv_bfloat162 v = kScaled ? __floats2bfloat162_rn(__fmul_rn(lo, scale), __fmul_rn(hi, scale))
+                                   : __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 // 32 accumulator columns of this lane's TMEM row, times `scale`, rounded to bf16 and packed in
 // pairs: h[i] = column 2i (low half) and column 2i + 1 (high half).
+template <bool kScaled>
 __device__ __forceinline__ void tc_ld_32_bf16(uint32_t taddr, float scale, uint32_t h[16]) {
   uint32_t r[32];
   asm volatile(
@@ -323,9 +329,7 @@ __device__ __forceinline__ void tc_ld_32_bf16(uint32_t taddr, float scale, uint3
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const uint32_t lo = __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(__uint_as_float(r[2 * i]), scale)));
-    const uint32_t hi = __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(__uint_as_float(r[2 * i + 1]), scale)));
-    h[i] = lo | (hi << 16);
+    h[i] = pack_bf16<kScaled>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), scale);
   }
 }
 
@@ -340,6 +344,17 @@ __device__ __forceinline__ void tc_ld_16(uint32_t taddr, float v[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The same for 16 columns (fewer registers in flight).
+template <bool kScaled>
+__device__ __forceinline__ void tc_ld_16_bf16(uint32_t taddr, float scale, uint32_t h[8]) {
+  float v[16];
+  tc_ld_16(taddr, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    h[i] = pack_bf16<kScaled>(v[2 * i], v[2 * i + 1], scale);
+  }
 }
 
 // Shared-memory matrix descriptor (tcgen05 format): start, leading/stride byte offsets,
@@ -373,6 +388,10 @@ struct Ctl {
   int tile_begin, tile_end;   // this CTA's contiguous range of tiles
 };
 
+// A value that every lane of the warp holds alike, made known to the compiler as such: what follows from it
+// stays in the uniform registers that the tensor-core instructions take, without a move per operand.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Bounded wait: true when the phase completed; false on timeout or when another role aborted.
 __device__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status,
                              uint64_t limit_ns = kWaitTimeoutNs) {
@@ -399,25 +418,42 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, ok);
 }
 
+// Both barriers, polled together (the usual case, both complete, then costs one round trip).
+__device__ __forceinline__ bool wait_warp2(uint32_t bar_a, uint32_t par_a, uint32_t bar_b, uint32_t par_b,
+                                           volatile int* abort_flag, int* status) {
+  const bool a = mbar_try_wait(bar_a, par_a), b = mbar_try_wait(bar_b, par_b);
+  if (__all_sync(0xffffffffu, a && b)) return true;
+  return wait_warp(bar_a, par_a, abort_flag, status) && wait_warp(bar_b, par_b, abort_flag, status);
+}
+
 // One tile of this CTA: expert, n-tile, first routed row and number of rows.
 struct TileDesc {
   int e, nt, r0, valid;
 };
 
 // Largest e with pref[e] <= t (pref[0] = 0, pref[E] = total tiles), then the tile's rows.
-__device__ __forceinline__ TileDesc decode_tile(int t, const int* pref, const int* offs, int E, int BN) {
+// even: the expert's token tiles share its rows evenly, in whole MMA steps of 16 tokens.
+__device__ __forceinline__ TileDesc decode_tile(int t, const int* pref, const int* offs, int E, int BN, bool even) {
   int lo = 0, hi = E;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (pref[mid] <= t) lo = mid; else hi = mid;
   }
   const int local = t - pref[lo];
-  const int mte = (offs[lo + 1] - offs[lo] + BN - 1) / BN;
+  const int rows = offs[lo + 1] - offs[lo];
+  const int mte = (rows + BN - 1) / BN;
   TileDesc d;
   d.e = lo;
+  if (mte == 1) {   // (no divisions: this runs before the launch's first copy)
+    d.nt = local;
+    d.r0 = offs[lo];
+    d.valid = rows;
+    return d;
+  }
+  const int step = even ? ((rows + mte - 1) / mte + 15) & ~15 : BN;
   d.nt = local / mte;
-  d.r0 = offs[lo] + (local % mte) * BN;
-  d.valid = min(BN, offs[lo + 1] - d.r0);
+  d.r0 = offs[lo] + (local % mte) * step;
+  d.valid = max(min(step, offs[lo + 1] - d.r0), 0);
   return d;
 }
 
@@ -434,23 +470,27 @@ __device__ __forceinline__ TileDesc decode_tile(int t, const int* pref, const in
 //    tried for the load balance of heavy token tiles, measured slower than the plain one.
 constexpr int kSchedRoundRobin = 0;
 constexpr int kSchedRuns = 1;
+//  kSchedRotate: round-robin whose rounds each start one unit further on.  Where experts have, say, one full
+//    and one short token tile, plain round-robin over an even number of units hands some units only full
+//    ones.
+constexpr int kSchedRotate = 2;
 
 // `unit` / `nunits`: this CTA's index and the number of CTAs, or for CTA pairs the pair's index
 // and the number of pairs (both CTAs of a pair take the same tiles).
 __device__ __forceinline__ int tile_of(int j, int sched, int tb, int unit, int nunits) {
   if (sched == kSchedRuns) return tb + j;
-  return j * nunits + unit;
+  return j * nunits + (sched == kSchedRotate ? (unit + j) % nunits : unit);
 }
 
 // The j-th tile of this CTA: from the shared-memory table filled at set-up, or decoded on the
 // spot past its capacity.
 __device__ __forceinline__ TileDesc my_tile(int j, const int4* table, int tcap, const int* pref, const int* offs,
-                                            int E, int BN, int sched, int tb, int unit, int nunits) {
+                                            int E, int BN, bool even, int sched, int tb, int unit, int nunits) {
   if (j < tcap) {
     const int4 v = table[j];
     return TileDesc{v.x, v.y, v.z, v.w};
   }
-  return decode_tile(tile_of(j, sched, tb, unit, nunits), pref, offs, E, BN);
+  return decode_tile(tile_of(j, sched, tb, unit, nunits), pref, offs, E, BN, even);
 }
 
 // Tile schedule: every CTA takes a contiguous run of tiles (expert-major, then n-tile, then token
@@ -477,33 +517,34 @@ __device__ __forceinline__ int tile_at_cost(long long target, const long long* c
   return pref[lo] + (int)(nt * mte + tt);
 }
 
-// 256-wide K chunks per ring stage: short token tiles take longer stages (fewer waits per weight
-// byte); 128-token tiles keep two-chunk stages, also on CTA pairs (three-chunk stages, three of
-// them in shared memory, measured slower than five two-chunk stages).  Wide pair tiles: two-chunk
-// stages for the sparse weights (three 62 KB stages; six one-chunk stages measured slower), one
-// chunk for the dense control's larger blocks.  The microscaled 4-bit formats follow the dense
-// control; with 8-bit activations a chunk already takes twice the shared memory, so one per stage.
-__host__ __device__ constexpr int stage_chunks(int fmt, int BN, bool glu, int cg, bool wide = false) {
-  return fmt == kFmtMx8 ? 1
-         : wide         ? (fmt == kFmtSparse ? 2 : 1)
-         : glu          ? 2
-                        : fmt == kFmtSparse ? (BN <= 32 ? 3 : 2) : (BN <= 32 ? 2 : 1);
-}
-// Format constants: 512-byte scale atoms per 256-wide chunk, shared-memory bytes of a weight chunk
-// block, activation bytes per row and chunk, and weight bits per 32 x 8 (= bytes per 32 weights).
-__host__ __device__ constexpr bool fmt_mx(int fmt) { return fmt == kFmtMx4 || fmt == kFmtMx8; }
-__host__ __device__ constexpr int fmt_sf_chunk(int fmt) { return fmt == kFmtDense ? 4 : 2; }
+// Format constants.  K values of a chunk (the packed weights' 256; half of it with 8-bit activations, whose
+// operands take a byte per value in shared memory, so that a chunk is 128 bytes of a row in every format),
+// 512-byte scale atoms per chunk, bytes of a weight chunk in a ring stage (the microscaled formats' scales
+// have a ring of their own) and bytes per 32 weights in HBM.
+__host__ __device__ constexpr int fmt_chunk_k(int fmt) { return fmt == kFmtMx8 ? kChunkK / 2 : kChunkK; }
+__host__ __device__ constexpr int fmt_sf_chunk(int fmt) { return fmt == kFmtDense ? 4 : fmt == kFmtMx8 ? 1 : 2; }
 __host__ __device__ constexpr int fmt_w_chunk(int fmt) {
-  return fmt == kFmtSparse ? kSparseChunkBytes
-         : fmt == kFmtDense ? kDenseChunkBytes
-         : fmt == kFmtMx4   ? kMxChunkBytes
-                            : kMxChunkBytes + kMxCodeBytes;
+  return fmt == kFmtSparse ? kSparseChunkBytes : fmt == kFmtDense ? kDenseChunkBytes : kMxCodeBytes;
 }
-__host__ __device__ constexpr int fmt_act_chunk(int fmt) { return fmt == kFmtMx8 ? 256 : 128; }
 __host__ __device__ constexpr int fmt_w_bytes32(int fmt) { return fmt == kFmtSparse ? 11 : fmt == kFmtDense ? 18 : 17; }
 __host__ __device__ constexpr int fmt_act_row(int fmt, int K) {   // activation codes + scales of a row
-  return K / 256 * (fmt_act_chunk(fmt) + 4 * fmt_sf_chunk(fmt));
+  return K / fmt_chunk_k(fmt) * (128 + 4 * fmt_sf_chunk(fmt));
 }
+// K chunks per ring stage: short token tiles take longer stages (fewer waits per weight byte); 128-token
+// tiles keep two-chunk stages, also on CTA pairs (three-chunk stages, three of them in shared memory,
+// measured slower than five two-chunk stages).  Wide pair tiles: two-chunk stages for the sparse weights
+// (three 62 KB stages; six one-chunk stages measured slower), one chunk for the dense control's larger
+// blocks.  The microscaled formats follow the dense control.
+__host__ __device__ constexpr int stage_chunks(int fmt, int BN, bool glu, int cg, bool wide = false) {
+  return wide  ? (fmt == kFmtSparse ? 2 : 1)
+         : glu || fmt == kFmtMx8 ? 2
+         : fmt == kFmtSparse ? (BN <= 32 ? 3 : 2) : (BN <= 32 ? 2 : 1);
+}
+// 512-byte scale atoms that hold the scales of a tile's tokens (128 each)
+__host__ __device__ constexpr int sfb_atoms(int BN) { return BN > 128 ? 2 : 1; }
+// Columns of a TMEM set: the microscaled formats have no metadata and fill at most 32.
+__host__ __device__ constexpr uint32_t set_cols(int fmt) { return fmt_mx(fmt) ? 32 : 64; }
+__host__ __device__ constexpr uint32_t col_acc(int fmt) { return kNSets * set_cols(fmt); }   // first accumulator
 
 // Compile-time stage geometry of one (sparse/dense, token tile, SwiGLU, CTA group) instantiation.
 // With the SwiGLU epilogue a tile holds two weight n-tiles (gate rows nt*128.., up rows
@@ -514,45 +555,47 @@ __host__ __device__ constexpr int fmt_act_row(int fmt, int K) {   // activation 
 // half of the shared activation tile.
 template <int kFmt, int kBN, bool kGLU = false, int kCG = 1, bool kWide = false>
 struct Geo {
-  static_assert(kCG == 1 || (kCG == 2 && !kGLU && kBN == 128), "CTA pairs: 128-token tiles, plain epilogue");
+  static_assert(kCG == 1 || (kCG == 2 && !kGLU && kBN >= 128), "CTA pairs: tiles of 128 tokens or more, plain epilogue");
+  static_assert(kBN <= 128 || (kWide && fmt_mx(kFmt)), "192-token tiles: wide pair tiles of the microscaled formats");
   static_assert(!kWide || kCG == 2, "wide tiles run on CTA pairs");
   static constexpr bool kSparse = kFmt == kFmtSparse;
   static constexpr bool kMx = fmt_mx(kFmt);
   static constexpr int kNT = (kGLU || kWide) ? 2 : 1;              // weight n-tiles per tile (per CTA)
   static constexpr int kKbLogical = kSparse ? 128 : kFmt == kFmtMx8 ? 32 : 64;   // logical K per MMA
-  static constexpr int kKbPerChunk = kChunkK / kKbLogical;         // MMAs per chunk: 2 sparse, 4, 8 with 8-bit tokens
+  static constexpr int kCK = fmt_chunk_k(kFmt);                    // K values of a chunk
+  static constexpr int kKbPerChunk = kCK / kKbLogical;             // MMAs per chunk: 2 sparse, else 4
   static constexpr int kSfPerChunk = fmt_sf_chunk(kFmt);           // scale atoms per chunk
   static constexpr int kMmaPerSf = kKbPerChunk / kSfPerChunk;      // MMAs that share an atom (1 for NVFP4)
   static constexpr int kSfIdStep = 4 / kMmaPerSf;                  // scale bytes each of them uses
-  // 256-wide K chunks per stage: short token tiles take longer stages (fewer waits per weight byte)
   static constexpr int kCPS = stage_chunks(kFmt, kBN, kGLU, kCG, kWide);
   static constexpr int kSfps = kCPS * kSfPerChunk;                 // scale atoms per stage
   static constexpr int kCB = fmt_w_chunk(kFmt);                    // weight chunk block in shared memory
   static constexpr int kCBMeta = 8192;                             // metadata offset in a chunk block
-  static constexpr int kCBScale = kSparse ? 10240 : kCB - 512 * kSfPerChunk;   // scale atoms offset in a chunk block
+  static constexpr int kCBScale = kSparse ? 10240 : kCB - 2048;    // scale atoms offset in a chunk block (NVFP4)
   static constexpr int kBRows = kBN / kCG;                         // token rows this CTA stages
-  static constexpr int kHalves = kFmt == kFmtMx8 ? 2 : 1;          // 128-byte wide token tiles per chunk
-  static constexpr int kBChunk = kBRows * 128 * kHalves;           // activation codes per chunk
+  static constexpr int kBChunk = kBRows * 128;                     // activation codes per chunk
+  static constexpr int kSfbA = sfb_atoms(kBN);                     // scale atoms of the tokens per k-block
   static constexpr int kOffW = kCPS * kBChunk;                     // stage layout: B chunks | W blocks | SFB
   static constexpr int kOffSFB = kOffW + kNT * kCPS * kCB;
-  static constexpr int kStage = (kOffSFB + kSfps * 512 + 1023) / 1024 * 1024;
+  static constexpr int kStage = (kOffSFB + (kMx ? 0 : kSfps * 512) + 1023) / 1024 * 1024;
+  // microscaled formats: a scale ring stage, [weight n-tile][atom], then [128 tokens][atom]
+  static constexpr int kScaleStage = kMx ? (kNT + kSfbA) * kSfps * 512 : 0;
+  static constexpr int kScaleOffB = kNT * kSfps * 512;
   static constexpr int kMetaCols = kSparse ? 4 * kCPS * kNT : 0;   // TMEM set: meta | SFA | SFB
   static constexpr int kColSFA = kMetaCols;
   static constexpr int kColSFB = kMetaCols + 4 * kSfps * kNT;
-  static constexpr int kSetUsed = kColSFB + 4 * kSfps;
+  static constexpr int kSetUsed = kColSFB + 4 * kSfbA * kSfps;
+  static constexpr uint32_t kSetCols = set_cols(kFmt), kColAcc = col_acc(kFmt);
   static constexpr uint32_t kBStep = kSparse ? 64 : 32;            // B bytes per row per MMA
   static constexpr int kBoxH = kBRows < 32 ? kBRows : 32;          // token rows per TMA box
   static constexpr int kAccStride = kBN < 32 ? 32 : kBN;
   static_assert(kSetUsed <= (int)kSetCols, "TMEM set too small");
+  static_assert(kColAcc + kNT * kAccStride <= kTmemCols, "TMEM too small for one accumulator buffer");
   // Operand A / B shared-memory descriptors' offsets of MMA h of a chunk: the NVFP4 weights are stored
   // as the MMA's core matrices, 4096 bytes per MMA; the microscaled weights and all tokens are 128-byte
-  // swizzled rows, of which an MMA takes kBStep bytes (8-bit tokens: two row tiles per chunk).
-  __device__ static constexpr uint32_t a_off(int h) {
-    return !kMx ? 4096u * h : kHalves == 2 ? (h / 4) * (uint32_t)kMxCodeBytes + 32u * (h % 4) : 32u * h;
-  }
-  __device__ static constexpr uint32_t b_off(int h) {
-    return kHalves == 2 ? (h / 4) * (uint32_t)(kBRows * 128) + 32u * (h % 4) : kBStep * h;
-  }
+  // swizzled rows, of which an MMA takes kBStep bytes.
+  __device__ static constexpr uint32_t a_off(int h) { return kMx ? 32u * h : 4096u * h; }
+  __device__ static constexpr uint32_t b_off(int h) { return kBStep * h; }
 };
 
 // kCG = 2: launched as clusters of two CTAs (a CTA pair on two SMs) that run 256-row weight tiles
@@ -639,27 +682,30 @@ __device__ void combine_tokens(const GemmParams& p, volatile int* abort_flag) {
 }
 
 template <int kFmt, int kBN, bool kGLU, int kCG, bool kNative = false, bool kWide = false>
-__global__ void __launch_bounds__(gemm_threads(kWide), 1)
+__global__ void __launch_bounds__(gemm_threads(kFmt, kWide), 1)
 grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant__ CUtensorMap tmap_b64,
                     const __grid_constant__ CUtensorMap tmap_sfb, const __grid_constant__ CUtensorMap tmap_w,
                     const GemmParams p) {
   using G = Geo<kFmt, kBN, kGLU, kCG, kWide>;
   constexpr bool kSparse = G::kSparse, kMx = G::kMx;
-  constexpr int kThreads = gemm_threads(kWide);
+  constexpr int kThreads = gemm_threads(kFmt, kWide);
   constexpr bool kPair = kCG == 2;
+  constexpr bool kEven = kMx && kBN >= 128;   // (shorter tiles: the schedule by bytes counts full ones)
   static_assert(!kNative || (kFmt == kFmtDense && kBN == 128 && !kGLU && kCG == 1), "native orientation: dense, 128 tokens");
   extern __shared__ uint8_t smem_raw[];
   // NT: weight n-tiles; tiles run over NT / (kNT * kCG) columns (the gate n-tiles with the SwiGLU
   // epilogue, n-tile pairs for CTA pairs)
-  const int E = p.E, NT = p.N / kTileN, NTt = NT / (G::kNT * kCG), KC = p.K / kChunkK;
+  const int E = p.E, NT = p.N / kTileN, NTt = kMx ? ceil_div_i(NT, G::kNT * kCG) : NT / (G::kNT * kCG), KC = p.K / G::kCK;
   const uint32_t rank = kPair ? cluster_ctarank() : 0u;         // this CTA's rank in its pair
   const int unit = kPair ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
   const int nunits = kPair ? (int)(gridDim.x >> 1) : (int)gridDim.x;
-  const int S = p.stages, NACC = p.nacc;
+  const int S = p.stages, NACC = kWide ? 1 : p.nacc;   // (a wide tile's two accumulators fill TMEM)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base + (size_t)S * G::kStage);
-  // bars: full[S], empty[S], tfull[kNSets], accf[NACC], acce[NACC], drain, never (test hook)
-  const int nbars = 2 * S + kNSets + 2 * NACC + 2;
+  const uint32_t scale_ring = smem_u32(base) + (uint32_t)(S * G::kStage);   // microscaled formats
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + (size_t)S * G::kStage + (kMx ? kScaleRing * G::kScaleStage : 0));
+  // bars: full[S], empty[S], tfull[kNSets], accf[NACC], acce[NACC], drain, never (test hook),
+  // microscaled formats also sfull[kScaleRing], sempty[kScaleRing]
+  const int nbars = 2 * S + kNSets + 2 * NACC + 2 + (kMx ? 2 * kScaleRing : 0);
   Ctl* ctl = reinterpret_cast<Ctl*>(bars + nbars);
   int* offs = reinterpret_cast<int*>(ctl + 1);   // [E+1]
   int* pref = offs + (E + 1);                    // [E+1]
@@ -671,7 +717,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
   uint8_t* ostage = reinterpret_cast<uint8_t*>(ttab + p.tcap);   // [4][kOutStageBytes or kGluStageBytes]
   volatile int* abort_flag = &ctl->abort;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t bar0 = smem_u32(bars);
   const uint32_t sbase = smem_u32(base);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -681,6 +727,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
   auto acce_bar = [&](int a) { return bar0 + 8u * (2 * S + kNSets + NACC + a); };
   const uint32_t drain_bar = bar0 + 8u * (2 * S + kNSets + 2 * NACC);
   const uint32_t never_bar = drain_bar + 8u;
+  auto sfull_bar = [&](int s) { return never_bar + 8u * (1 + s); };
+  auto sempty_bar = [&](int s) { return never_bar + 8u * (1 + kScaleRing + s); };
 
   // ---- set-up: barriers, TMEM, tile schedule, tensor scales (global memory only after pdl_wait)
   pdl_launch_dependents();
@@ -696,6 +744,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
     for (int a = 0; a < NACC; ++a) { mbar_init(accf_bar(a), 1); mbar_init(acce_bar(a), 4 * kCG * (kWide ? 2 : 1)); }
     mbar_init(drain_bar, 1);
     mbar_init(never_bar, 1);
+    if (kMx)
+      for (int s = 0; s < kScaleRing; ++s) { mbar_init(sfull_bar(s), 1); mbar_init(sempty_bar(s), 4); }
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -716,15 +766,6 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
     }
   }
   pdl_wait();
-  // expert offsets, clamped to [0, R] so a corrupt array can never send a copy or a store out
-  // of bounds (a decreasing pair makes that expert empty, see below)
-  bool bad = false;
-  for (int i = threadIdx.x; i <= E; i += blockDim.x) {
-    int v = __ldg(p.off + i);
-    if (v < 0 || v > p.R) { bad = true; v = v < 0 ? 0 : p.R; }
-    offs[i] = v;
-    if (i < E) wsc[i] = kMx ? 1.0f : __ldg(p.w_scale + i);
-  }
   if (kGLU) {
     // h scale entries that refer to rows >= R (no tile writes them): zero, shared by the CTAs
     const int r_lo = p.R > 96 ? p.R - 96 : 0, span = p.rcap - r_lo, kbh = p.N / 256;
@@ -733,44 +774,56 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
       if (rr + 32 * cc >= p.R) *reinterpret_cast<uint32_t*>(p.h_scales + ((size_t)kb * p.rcap + rr) * 16 + cc * 4) = 0u;
     }
   }
-  __syncthreads();
-  {
-    // chunked exclusive scan of tiles_e = ceil(rows_e / BN) * NTt over E experts
-    const int per = (E + kThreads - 1) / kThreads;
-    const int e0 = threadIdx.x * per, e1 = min(e0 + per, E);
-    int local = 0;
-    for (int e = e0; e < e1; ++e) {
-      int rows = offs[e + 1] - offs[e];
-      if (rows < 0) { bad = true; rows = 0; }
-      local += ((rows + kBN - 1) / kBN) * NTt;
-    }
-    int incl = local;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      int n = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += n;
-    }
-    __shared__ int wsum[kThreads / 32];
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before += wsum[w];
-    int run = before + incl - local;
-    for (int e = e0; e < e1; ++e) {
-      pref[e] = run;
-      int rows = offs[e + 1] - offs[e];
-      if (rows < 0) rows = 0;
-      run += ((rows + kBN - 1) / kBN) * NTt;
-    }
-    if (threadIdx.x == kThreads - 1) pref[E] = before + incl;
+  // expert offsets, clamped to [0, R] so a corrupt array can never send a copy or a store out
+  // of bounds (a decreasing pair makes that expert empty), and the exclusive scan pref of
+  // tiles_e = ceil(rows_e / BN) * NTt: a chunk of experts per thread, the threads' sums by warp.
+  // (This runs once per launch, its instructions cold in the caches, so it is kept short: three
+  // block barriers in all, and every thread works out the totals it needs itself.)
+  bool bad = false;
+  auto offset_at = [&](int i) {
+    const int v = __ldg(p.off + i);
+    if (v < 0 || v > p.R) bad = true;
+    return min(max(v, 0), p.R);
+  };
+  auto tiles_of = [&](int e) { return (max(offs[e + 1] - offs[e], 0) + kBN - 1) / kBN * NTt; };
+  const int per = (E + kThreads - 1) / kThreads;
+  const int e0 = min((int)threadIdx.x * per, E), e1 = min(e0 + per, E);
+  int local = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int lo = offset_at(e), hi = offset_at(e + 1);
+    if (hi < lo) bad = true;
+    offs[e] = lo;
+    if (e == E - 1) offs[E] = hi;
+    if (!kMx) wsc[e] = __ldg(p.w_scale + e);
+    local += (max(hi - lo, 0) + kBN - 1) / kBN * NTt;
   }
+  __shared__ int wsum[kThreads / 32];
+  int incl = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += n;
+  }
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  int run = incl - local, total_tiles = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const int n = wsum[w];
+    if (w < warp) run += n;
+    total_tiles += n;
+  }
+  for (int e = e0; e < e1; ++e) {
+    pref[e] = run;
+    run += tiles_of(e);
+  }
+  if (threadIdx.x == 0) pref[E] = total_tiles;
+  if (bad) set_status(p.status, GSG_ERR_BAD_ROUTING);
   // bytes per tile: weights wc, plus ac per token row (codes, scales, output row segment)
   const long long wc = (long long)G::kNT * kCG * kTileN * p.K * fmt_w_bytes32(kFmt) / 32;
   const long long ac = fmt_act_row(kFmt, p.K) + (long long)G::kNT * kCG * kTileN * (p.y_f32 ? 4 : 2);
   if (p.sched == kSchedRuns) {   // (only the byte-balanced schedule reads the costs; uniform branch)
-    // chunked exclusive scan of cost_e = NTt * (ceil(rows_e / BN) * wc + rows_e * ac)
-    const int per = (E + kThreads - 1) / kThreads;
-    const int e0 = threadIdx.x * per, e1 = min(e0 + per, E);
+    // the same scan of cost_e = NTt * (ceil(rows_e / BN) * wc + rows_e * ac)
     long long local = 0;
     for (int e = e0; e < e1; ++e) {
       const int rows = max(offs[e + 1] - offs[e], 0);
@@ -792,30 +845,34 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
       const int rows = max(offs[e + 1] - offs[e], 0);
       run += (long long)NTt * (((rows + kBN - 1) / kBN) * wc + rows * ac);
     }
-    if (threadIdx.x == kThreads - 1) costp[E] = run;
+    if (e0 < E && e1 == E) costp[E] = run;
   }
-  if (bad) set_status(p.status, GSG_ERR_BAD_ROUTING);
   __syncthreads();
-  const int total_tiles = pref[E];
-  if (threadIdx.x == 0) {
-    const int b = unit, G_ = nunits;
-    if (p.sched == kSchedRuns) {
+  int tb = 0, n_my;
+  if (p.sched == kSchedRuns) {
+    if (threadIdx.x == 0) {
       const long long C = costp[E];
-      const int tb = tile_at_cost(C * b / G_, costp, pref, offs, E, kBN, wc, ac);
-      const int te = b == G_ - 1 ? total_tiles : tile_at_cost(C * (b + 1) / G_, costp, pref, offs, E, kBN, wc, ac);
-      ctl->tile_begin = tb;
-      ctl->tile_end = te;
-    } else {
-      ctl->tile_begin = 0;
-      ctl->tile_end = b < total_tiles ? (total_tiles - b + G_ - 1) / G_ : 0;
+      ctl->tile_begin = tile_at_cost(C * unit / nunits, costp, pref, offs, E, kBN, wc, ac);
+      ctl->tile_end = unit == nunits - 1 ? total_tiles
+                                         : tile_at_cost(C * (unit + 1) / nunits, costp, pref, offs, E, kBN, wc, ac);
     }
+    __syncthreads();
+    tb = uniform(ctl->tile_begin);
+    n_my = uniform(ctl->tile_end) - tb;
+  } else {
+    // total / nunits without the integer division's instructions (a quotient below 2^22 is at most one off)
+    int rounds = total_tiles >> 22 != 0 ? total_tiles / nunits
+                                        : __float2int_rz(__fdividef((float)total_tiles, (float)nunits));
+    int rest = total_tiles - rounds * nunits;
+    if (rest < 0) { --rounds; rest += nunits; }
+    if (rest >= nunits) { ++rounds; rest -= nunits; }
+    // this unit's place in the last round
+    const int at = p.sched == kSchedRotate ? (unit + rounds) % nunits : unit;
+    n_my = uniform(rounds + (at < rest ? 1 : 0));
   }
-  __syncthreads();
-  const int tb = ctl->tile_begin;
   // this CTA's tiles, decoded once
-  const int n_my = ctl->tile_end - tb;
   for (int j = threadIdx.x; j < n_my && j < p.tcap; j += blockDim.x) {
-    const TileDesc d = decode_tile(tile_of(j, p.sched, tb, unit, nunits), pref, offs, E, kBN);
+    const TileDesc d = decode_tile(tile_of(j, p.sched, tb, unit, nunits), pref, offs, E, kBN, kEven);
     ttab[j] = make_int4(d.e, d.nt, d.r0, d.valid);
   }
   tc_fence_before();
@@ -825,9 +882,50 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
     __syncthreads();
   }
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem_base;
+  const uint32_t tmem = (uint32_t)uniform((int)ctl->tmem_base);
 
-  if (warp == 0 || warp == 2) {
+  if (kMx && warp == kThreads / 32 - 1) {
+    // =============================== scale producer (microscaled formats): the scale atoms of each stage,
+    // in a ring of their own that runs ahead of the operands', so that the loader warps have them in TMEM
+    // when the operands land
+    int s = 0, g = 0;
+    uint32_t ph = 0;
+    for (int j = 0; j < n_my && !*abort_flag; ++j) {
+      const TileDesc c = my_tile(j, ttab, p.tcap, pref, offs, E, kBN, kEven, p.sched, tb, unit, nunits);
+      constexpr int kCPB = kChunkK / G::kCK;     // chunks of a packed chunk block
+      const int KB = KC / kCPB;
+      // (n-tiles past the last, in a wide tile at the end of N, are the last one again; see the epilogue)
+      const int nt0 = min(c.nt * kCG * G::kNT + (int)rank, NT - 1), nt1 = min(nt0 + kCG, NT - 1);
+      const size_t wblk = ((size_t)c.e * NT + nt0) * KB, wup = (size_t)(nt1 - nt0) * KB;
+      bool ok = true;
+      for (int kc = 0; kc < KC; kc += G::kCPS) {
+        const int nch = KC - kc >= G::kCPS ? G::kCPS : KC - kc;
+        if (!wait_warp(sempty_bar(s), ph ^ 1u, abort_flag, p.status)) { ok = false; break; }
+        const uint32_t st = scale_ring + (uint32_t)(s * G::kScaleStage), fb = sfull_bar(s);
+        mbar_arrive_expect_tx(fb, (uint32_t)(G::kNT * nch * G::kSfPerChunk * 512 + G::kSfbA * G::kSfps * 512));
+        // lane t * blocks + b copies weight n-tile t's atoms of the stage's b-th block (blocks of two chunks
+        // with 8-bit activations, of which a stage holds one half or both); the last lanes copy the tokens'
+        const int blocks = (nch + kCPB - 1) / kCPB, t = lane / blocks, b = lane - t * blocks;
+        bulk_g2s_lane(lane < G::kNT * blocks, st + (t * G::kSfps + b * kCPB * G::kSfPerChunk) * 512,
+                      p.w_packed + (wblk + (t == 0 ? 0 : wup) + kc / kCPB + b) * kMxChunkBytes +
+                          kMxCodeBytes + kc % kCPB * (G::kSfPerChunk * 512),
+                      (nch < kCPB ? nch : kCPB) * (G::kSfPerChunk * 512u), fb);
+        tma_load_2d_lane(lane > 31 - G::kSfbA, st + G::kScaleOffB + (31 - lane) * (G::kSfps * 512), &tmap_sfb,
+                         4 * (c.r0 + 128 * (31 - lane)), kc * G::kSfPerChunk, fb);
+        ++g;
+        if (++s == kScaleRing) { s = 0; ph ^= 1u; }
+      }
+      if (!ok) break;
+    }
+    if (*abort_flag && lane == 0) {   // as the operands' producers below
+      const uint64_t t0 = globaltimer_ns();
+      for (int g2 = g > kScaleRing ? g - kScaleRing : 0; g2 < g; ++g2) {
+        while (!mbar_try_wait(sfull_bar(g2 % kScaleRing), (uint32_t)(g2 / kScaleRing) & 1u) &&
+               globaltimer_ns() - t0 < kWaitTimeoutNs) {
+        }
+      }
+    }
+  } else if (warp == 0 || warp == 2) {
     // =============================== producers: warp 0 weights, warp 2 activations.  The copies of
     // a stage are issued from separate lanes (see bulk_g2s_lane): the TMA unit works through one
     // thread's copies one after another, so one lane issuing every copy would keep a single copy
@@ -836,20 +934,25 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
     int s = 0, g = 0;   // ring slot and stage counter
     uint32_t ph = 0;
     for (int j = 0; j < n_my && !*abort_flag; ++j) {
-      const TileDesc c = my_tile(j, ttab, p.tcap, pref, offs, E, kBN, p.sched, tb, unit, nunits);
+      const TileDesc c = my_tile(j, ttab, p.tcap, pref, offs, E, kBN, kEven, p.sched, tb, unit, nunits);
       // this CTA's first weight n-tile: tile c.nt spans n-tiles [c.nt * kCG * kNT, +kCG * kNT) of the
       // expert (SwiGLU: the gate n-tiles only), CTA r of a pair takes every other one from r
       constexpr int kPackedCB = kMx ? kMxChunkBytes : G::kCB;   // chunk block in the packed weights
-      const size_t wblk = ((size_t)c.e * NT + c.nt * kCG * (kWide ? 2 : 1) + rank) * KC;   // its first chunk block
+      constexpr int kCPB = kChunkK / G::kCK;     // chunks that a block holds (two with 8-bit activations)
+      const int KB = KC / kCPB;
+      const int nt0 = kMx ? min(c.nt * kCG * G::kNT + (int)rank, NT - 1) : c.nt * kCG * (kWide ? 2 : 1) + (int)rank;
+      const size_t wblk = ((size_t)c.e * NT + nt0) * KB;   // its first chunk block
       const uint8_t* wsrc = p.w_packed + wblk * kPackedCB;
       // its second n-tile: SwiGLU, the matching up n-tile; a wide pair tile, the next pair's
-      const size_t wup = (size_t)(kWide ? kCG : NT / 2) * KC;
+      const size_t wup = (size_t)(kMx ? min(kCG, NT - 1 - nt0) : kWide ? kCG : NT / 2) * KB;
       const uint8_t* wsrc_up = wsrc + wup * kPackedCB;
       // this CTA's token rows [r0, r0 + cnt): all of the tile's, or for a CTA pair the half of the
       // MMA's N = valid rounded up to 16 that this CTA supplies (rank 1: the upper half)
       const int nh = kPair ? ((c.valid + 15) & ~15) / 2 : kBN;
       const int r0 = c.r0 + (int)rank * nh;
       const int cnt = min(max(c.valid - (int)rank * nh, 0), nh);
+      // (the leader of a microscaled pair also announces the other CTA's rows)
+      const int cnt1 = kMx && kPair ? min(max(c.valid - nh, 0), nh) : 0;
       // token rows to fetch: whole 32-row boxes (BN <= 32: one box of BN rows), as few 64-row
       // boxes as possible for the larger tiles -- every TMA instruction costs the issuing warp
       const int rows = (cnt + G::kBoxH - 1) / G::kBoxH * G::kBoxH;
@@ -861,40 +964,43 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
         if (!wait_warp(empty_bar(s), ph ^ 1u, abort_flag, p.status)) { ok = false; break; }
         const uint32_t st = sbase + (uint32_t)s * G::kStage;
         const uint32_t fb = full_bar(s);
+        // microscaled pairs: both CTAs' copies complete on the leader's barrier, where the MMAs wait
+        const uint32_t cfb = kMx && kPair ? cluster_addr(fb, 0u) : fb;
         if (wprod) {
           // weights (+ metadata + weight scales): lane t * nch + ch copies chunk block ch of weight
           // n-tile t (t = 1: the SwiGLU up n-tile); lane 31 copies the activation scale atoms of the
           // whole tile's tokens from its first row (in both CTAs of a pair: each CTA's MMA share
           // needs the scales of all N token columns)
-          // (the 4-bit codes that a copy widens for 8-bit activations still count as they lie in HBM)
-          mbar_arrive_expect_tx(fb, (uint32_t)(G::kNT * nch * kPackedCB + G::kSfps * 512));
           if constexpr (kMx) {
-            // per chunk block: the 128 rows of codes (256 values; for 8-bit activations two copies of 128
-            // values, which the TMA widens to 128 bytes each), then the block's two scale atoms
-            const int u = lane / G::kHalves, half = lane % G::kHalves;
-            const int t = u / nch, ch = u - t * nch;
-            const int row = (int)((wblk + (t == 0 ? 0 : wup) + kc + ch) * kMxChunkRows);
-            const uint32_t dst = st + G::kOffW + (t * G::kCPS + ch) * G::kCB;
-            tma_load_2d_lane(u < G::kNT * nch, dst + half * kMxCodeBytes, &tmap_w, half * 128, row, fb);
-            const int v = lane - 16, tv = v / nch, cv = v - tv * nch;   // lanes 16 and up
-            bulk_g2s_lane(v >= 0 && v < G::kNT * nch, st + G::kOffW + (tv * G::kCPS + cv) * G::kCB + G::kCBScale,
-                          (tv == 0 ? wsrc : wsrc_up) + (size_t)(kc + cv) * kPackedCB + kMxCodeBytes, 1024u, fb);
+            // per chunk: the 128 rows of its codes (256 values, or for 8-bit activations the chunk's half of
+            // the block's, which the TMA widens to 128 bytes a row; it counts the bytes read)
+            if (rank == 0) mbar_arrive_expect_tx(fb, (uint32_t)(G::kNT * nch * (kMxCodeBytes / kCPB) * kCG));
+            const int t = lane / nch, ch = kc + lane - t * nch;
+            const int row = (int)((wblk + (t == 0 ? 0 : wup) + ch / kCPB) * kMxChunkRows);
+            const bool on = lane < G::kNT * nch;
+            const uint32_t dst = st + G::kOffW + (t * G::kCPS + ch - kc) * G::kCB;
+            if constexpr (kPair) tma_load_2d_lane_pair(on, dst, &tmap_w, ch % kCPB * G::kCK, row, cfb);
+            else tma_load_2d_lane(on, dst, &tmap_w, ch % kCPB * G::kCK, row, cfb);
           } else {
+            mbar_arrive_expect_tx(fb, (uint32_t)(G::kNT * nch * G::kCB + G::kSfps * 512));
             const int t = lane / nch, ch = lane - t * nch;
             bulk_g2s_lane(lane < G::kNT * nch, st + G::kOffW + (t * G::kCPS + ch) * G::kCB,
                           (t == 0 ? wsrc : wsrc_up) + (size_t)(kc + ch) * G::kCB, G::kCB, fb);
+            tma_load_2d_lane(lane == 31, st + G::kOffSFB, &tmap_sfb, 4 * c.r0, kc * G::kSfPerChunk, fb);
           }
-          tma_load_3d_lane(lane == 31, st + G::kOffSFB, &tmap_sfb, 0, c.r0, kc * G::kSfPerChunk, fb);
         } else {
-          // activation codes: lane ch * nb + b copies box b (64-row boxes first) of chunk ch (of 128-byte
-          // half ch of the stage's chunks for 8-bit activations)
-          mbar_arrive_expect_tx(fb, (uint32_t)(nch * G::kHalves * rows * 128));
+          // activation codes: lane ch * nb + b copies box b (64-row boxes first) of chunk ch
+          const int rows1 = (cnt1 + G::kBoxH - 1) / G::kBoxH * G::kBoxH;
+          if (!(kMx && kPair) || rank == 0) mbar_arrive_expect_tx(fb, (uint32_t)(nch * (rows + rows1) * 128));
           const int nb = n64 + n32;
           const int ch = nb > 0 ? lane / nb : 0, b = lane - ch * nb;
           const bool b64 = b < n64;
           const int roff = b64 ? 64 * b : 64 * n64 + (b - n64) * G::kBoxH;
-          tma_load_2d_lane(lane < nch * G::kHalves * nb, st + ch * (G::kBChunk / G::kHalves) + roff * 128,
-                           b64 ? &tmap_b64 : &tmap_b, (kc * G::kHalves + ch) * 128, r0 + roff, fb);
+          const uint32_t dst = st + ch * G::kBChunk + roff * 128;
+          if constexpr (kMx && kPair)
+            tma_load_2d_lane_pair(lane < nch * nb, dst, b64 ? &tmap_b64 : &tmap_b, (kc + ch) * 128, r0 + roff, cfb);
+          else
+            tma_load_2d_lane(lane < nch * nb, dst, b64 ? &tmap_b64 : &tmap_b, (kc + ch) * 128, r0 + roff, fb);
         }
         ++g;
         if (++s == S) { s = 0; ph ^= 1u; }
@@ -904,7 +1010,13 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
     if (*abort_flag && lane == 0) {
       // wait (2 s in all) for copies still landing in the stages this warp filled: the last S
       // before stage g (the first one it did not issue)
+      // (the second CTA of a microscaled pair has no barrier of its own for them: it gives them 10 ms, a
+      // thousand times what a copy takes, and leaves only after the leader's wait, at the cluster barrier)
       const uint64_t t0 = globaltimer_ns();
+      if (kMx && kPair && rank != 0)
+        while (globaltimer_ns() - t0 < 10000000ull) {
+        }
+      else
       for (int g2 = g > S ? g - S : 0; g2 < g; ++g2) {
         while (!mbar_try_wait(full_bar(g2 % S), (uint32_t)(g2 / S) & 1u) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
         }
@@ -929,8 +1041,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
             break;
           }
         }
-        if (!wait_warp(full_bar(s), ph, abort_flag, p.status)) { ok = false; break; }
-        const uint32_t st = sbase + (uint32_t)s * G::kStage;
+        if (!wait_warp(kMx ? sfull_bar(s) : full_bar(s), ph, abort_flag, p.status)) { ok = false; break; }
+        const uint32_t st = kMx ? scale_ring + (uint32_t)(s * G::kScaleStage) : sbase + (uint32_t)s * G::kStage;
         uint32_t r[G::kSetUsed];
         if (kSparse) {
 #pragma unroll
@@ -948,16 +1060,25 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
           if (kb < nch * G::kSfPerChunk) {
 #pragma unroll
             for (int t = 0; t < G::kNT; ++t) {
-              const uint32_t sfa = st + G::kOffW + (t * G::kCPS + kb / G::kSfPerChunk) * G::kCB + G::kCBScale +
-                                   (kb % G::kSfPerChunk) * 512;
+              const uint32_t sfa = kMx ? st + (t * G::kSfps + kb) * 512
+                                       : st + G::kOffW + (t * G::kCPS + kb / G::kSfPerChunk) * G::kCB + G::kCBScale +
+                                             (kb % G::kSfPerChunk) * 512;
               const int m = G::kColSFA + 4 * (t * G::kSfps + kb);
               lds128(sfa + lane * 16, r[m], r[m + 1], r[m + 2], r[m + 3]);
             }
-            lds128(st + G::kOffSFB + kb * 512 + lane * 16, r[G::kColSFB + 4 * kb], r[G::kColSFB + 4 * kb + 1],
-                   r[G::kColSFB + 4 * kb + 2], r[G::kColSFB + 4 * kb + 3]);
+#pragma unroll
+            for (int a = 0; a < G::kSfbA; ++a) {   // (tokens 128 and up: the next four columns)
+              const int m = G::kColSFB + 4 * (G::kSfbA * kb + a);
+              lds128(st + (kMx ? G::kScaleOffB : G::kOffSFB) + (a * G::kSfps + kb) * 512 + lane * 16, r[m], r[m + 1],
+                     r[m + 2], r[m + 3]);
+            }
           }
         }
-        tc_st_cols<G::kSetUsed>(tmem + tlane + (uint32_t)set * kSetCols, r);
+        if constexpr (kMx) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sempty_bar(s));   // the atoms are in registers
+        }
+        tc_st_cols<G::kSetUsed>(tmem + tlane + (uint32_t)set * G::kSetCols, r);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -967,39 +1088,39 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
         }
         ++i;
         if (++set == kNSets) set = 0;
-        if (++s == S) { s = 0; ph ^= 1u; }
+        if (++s == (kMx ? kScaleRing : S)) { s = 0; ph ^= 1u; }
       }
       if (!ok) break;
     }
   } else if (warp == 1) {
     // =============================== MMA issuer (whole warp, one elected lane issues); for a CTA
     // pair only the leader's, whose MMAs run on both SMs (the other CTA's warp 1 has no tiles)
-    int s = 0, set = 0, i = 0, acc = 0;
-    uint32_t ph = 0, aph = 0;   // ring phase, accumulator phase
+    int s = 0, set = 0, acc = 0;
+    uint32_t ph = 0, sph = 0, aph = 0;   // phases of the ring, the TMEM sets, the accumulators
     bool any = false;
     const int n_mma = rank == 0u ? n_my : 0;
     for (int j = 0; j < n_mma && !*abort_flag; ++j) {
-      const TileDesc c = my_tile(j, ttab, p.tcap, pref, offs, E, kBN, p.sched, tb, unit, nunits);
-      const uint32_t idesc = kMx ? make_idesc_mx(kFmt == kFmtMx8, (c.valid + 15) & ~15, kTileN * kCG)
+      const TileDesc c = my_tile(j, ttab, p.tcap, pref, offs, E, kBN, kEven, p.sched, tb, unit, nunits);
+      const int nval = uniform((c.valid + 15) & ~15);   // the MMA's N
+      const uint32_t idesc = kMx ? make_idesc_mx(kFmt == kFmtMx8, nval, kTileN * kCG)
                              : kNative ? make_idesc(false, kTileN, kBN)   // M = 128 tokens, N = 128 weight rows
-                                     : make_idesc(kSparse, (c.valid + 15) & ~15, kTileN * kCG);
+                                     : make_idesc(kSparse, nval, kTileN * kCG);
       if (p.stall_ns != 0ull && j == (n_mma > 1 ? 1 : 0) &&
           !wait_warp(never_bar, 0u, abort_flag, p.status, p.stall_ns))
         break;
       if (!wait_warp(acce_bar(acc), aph ^ 1u, abort_flag, p.status)) break;
       tc_fence_after();
-      const uint32_t d_tmem = tmem + kColAcc + (uint32_t)(acc * G::kNT * G::kAccStride);
+      const uint32_t d_tmem = tmem + G::kColAcc + (uint32_t)(acc * G::kNT * G::kAccStride);
       bool ok = true;
       for (int kc = 0; kc < KC; kc += G::kCPS) {
         const int nch = KC - kc >= G::kCPS ? G::kCPS : KC - kc;
-        if (!wait_warp(full_bar(s), ph, abort_flag, p.status) ||
-            !wait_warp(tfull_bar(set), (uint32_t)(i / kNSets) & 1u, abort_flag, p.status)) {
+        if (!wait_warp2(full_bar(s), ph, tfull_bar(set), sph, abort_flag, p.status)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t st = sbase + (uint32_t)s * G::kStage;
-        const uint32_t tset = tmem + (uint32_t)set * kSetCols;
+        const uint32_t tset = tmem + (uint32_t)set * G::kSetCols;
 #pragma unroll
         for (int ch = 0; ch < G::kCPS; ++ch) {
           if (ch < nch) {
@@ -1014,7 +1135,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
                 const uint64_t adesc = kMx ? smem_desc(aaddr, 16, 1024, 2) : smem_desc(aaddr, 128, 256, 0);
                 const uint32_t d = d_tmem + (uint32_t)(t * G::kAccStride);
                 const int kt = t * G::kSfps + kbi;
-                const uint32_t sfa = tset + G::kColSFA + 4 * kt, sfb = tset + G::kColSFB + 4 * kbi;
+                const uint32_t sfa = tset + G::kColSFA + 4 * kt, sfb = tset + G::kColSFB + 4 * G::kSfbA * kbi;
                 if constexpr (kMx)
                   tc_mma_mx<kFmt == kFmtMx8, kPair>(
                       d, adesc, bdesc, idesc | idesc_sf((h % G::kMmaPerSf) * G::kSfIdStep),
@@ -1036,8 +1157,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
         if constexpr (kPair) tc_commit_pair(empty_bar(s), 3);   // the stage is free in both CTAs
         else tc_commit(empty_bar(s));
         any = true;
-        ++i;
-        if (++set == kNSets) set = 0;
+        if (++set == kNSets) { set = 0; sph ^= 1u; }
         if (++s == S) { s = 0; ph ^= 1u; }
       }
       if (!ok) break;
@@ -1062,12 +1182,15 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
     int acc = 0;
     uint32_t aph = 0;
     for (int j = 0; j < n_my; ++j) {
-      const TileDesc c = my_tile(j, ttab, p.tcap, pref, offs, E, kBN, p.sched, tb, unit, nunits);
-      const int r0 = c.r0, valid = c.valid;
+      const TileDesc c = my_tile(j, ttab, p.tcap, pref, offs, E, kBN, kEven, p.sched, tb, unit, nunits);
+      // (an n-tile past the last, in a microscaled format's wide tile at the end of N, is computed like any
+      // other and not stored)
+      const bool past = kMx && kWide && (2 * c.nt + (warp >= 11 ? 1 : 0)) * kCG + (int)rank >= NT;
+      const int r0 = c.r0, valid = past ? 0 : c.valid;
       if (!wait_warp(accf_bar(acc), aph, abort_flag, p.status)) break;
       tc_fence_after();
-      const float scale = __fmul_rn(sx, wsc[c.e]);
-      const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + kColAcc + (uint32_t)(acc * G::kNT * G::kAccStride);
+      const float scale = kMx ? 1.0f : __fmul_rn(sx, wsc[c.e]);
+      const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + G::kColAcc + (uint32_t)(acc * G::kNT * G::kAccStride);
       bool released = false;   // the accumulator already handed back to the MMA warp
       if constexpr (kNative) {
         // lane = token 32q + lane of the tile, columns = the n-tile's 128 features: each lane scales
@@ -1163,17 +1286,83 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
       const uint32_t obuf_s = smem_u32(obuf);
       // the tile's n-tiles: a wide pair tile's second one goes to warps 11..14
       const int u_begin = kWide ? (warp >= 11 ? 1 : 0) : 0, u_end = kWide ? u_begin + 1 : G::kNT;
-      if constexpr (kBN == 128 && G::kNT == 1 + (kWide ? 1 : 0)) {
+      if constexpr (kBN >= 128 && G::kNT == 1 + (kWide ? 1 : 0)) {
         if (!p.y_f32 && p.perm_src == nullptr) {
-          // bf16 output of a 128-token tile (one n-tile per warp): the warp's whole accumulator
+          // bf16 output of a tile of 128 tokens or more (one n-tile per warp): the warp's whole accumulator
           // block in 32-column TMEM loads, held as packed bf16, and the accumulator released
           // before any store, so the MMA warp's next tile waits for the loads, not for the stores
           const uint32_t tcol = taddr + (uint32_t)(u_begin * G::kAccStride);
-          const size_t col0 = ((size_t)c.nt * kCG * G::kNT + u_begin * kCG + rank) * kTileN + 32 * q;
-          uint32_t hb[64];
+          const int col0 = (c.nt * kCG * G::kNT + u_begin * kCG + (int)rank) * kTileN + 32 * q;
+          // tokens t0 .. t0 + 31 of the tile, h16[i] this lane's feature of tokens t0 + 2i (low half) and
+          // t0 + 2i + 1: neighbouring lanes trade halves, so that each holds two features of one token, and
+          // the block crosses the warp's buffer as [token][feature] in 32-bit words (conflict-free)
+          // (NVFP4, whose extra scaling leaves fewer registers: sixteen tokens at a time, a half word each)
+          auto store32 = [&](int t0, const uint32_t* h16) {
+            if constexpr (!kMx) {
 #pragma unroll
-          for (int h = 0; h < 4; ++h)
-            if (32 * h < valid) tc_ld_32_bf16(tcol + 32u * h, scale, hb + 16 * h);   // warp-uniform
+              for (int g = 0; g < 2; ++g) {
+                if (t0 + 16 * g < valid) {
+#pragma unroll
+                  for (int j = 0; j < 16; j += 2) {
+                    const uint32_t w = h16[8 * g + j / 2];
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(obuf_s + (uint32_t)(j * 64 + lane * 2)),
+                                 "h"((unsigned short)(w & 0xffffu)) : "memory");
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(obuf_s + (uint32_t)((j + 1) * 64 + lane * 2)),
+                                 "h"((unsigned short)(w >> 16)) : "memory");
+                  }
+                  __syncwarp();
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {   // 16 tokens x 4 chunks of 16 B
+                    const int ci = lane + 32 * k, tok = ci >> 2, part = ci & 3;
+                    if (t0 + 16 * g + tok < valid) {
+                      uint32_t a, b, cc, d;
+                      lds128(obuf_s + (uint32_t)(tok * 64 + part * 16), a, b, cc, d);
+                      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.Y) + (size_t)(r0 + t0 + 16 * g + tok) * p.N +
+                                                col0 + part * 8) = make_uint4(a, b, cc, d);
+                    }
+                  }
+                  __syncwarp();
+                }
+              }
+              return;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t other = __shfl_xor_sync(0xffffffffu, h16[i], 1);
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(obuf_s + (uint32_t)((2 * i + (lane & 1)) * 64 + (lane >> 1) * 4)),
+                           "r"(__byte_perm(h16[i], other, (lane & 1) ? 0x3276 : 0x5410)) : "memory");
+            }
+            __syncwarp();
+            __nv_bfloat16* Yl = static_cast<__nv_bfloat16*>(p.Y) + (size_t)(r0 + t0 + (lane >> 2)) * p.N + col0 + (lane & 3) * 8;
+#pragma unroll 2
+            for (int k = 0; k < 4; ++k) {   // 32 tokens x 4 chunks of 16 B
+              uint32_t a, b, cc, d;
+              lds128(obuf_s + (uint32_t)(k * 512 + lane * 16), a, b, cc, d);
+              if (t0 + 8 * k + (lane >> 2) < valid)
+                *reinterpret_cast<uint4*>(Yl + (size_t)(8 * k) * p.N) = make_uint4(a, b, cc, d);
+            }
+            __syncwarp();
+          };
+          constexpr int kHold = kBN < 160 ? kBN : 160;   // (what a thread's 128 registers hold without spills)
+          if constexpr (kHold < kBN) {
+            static_assert(kBN - kHold == 32, "one block of 32 tokens before the rest");
+            if (kHold < valid) {
+              uint32_t h16[16];
+              tc_ld_32_bf16<!kMx>(tcol + kHold, scale, h16);
+              store32(kHold, h16);
+            }
+          }
+          uint32_t hb[kHold / 2];
+#pragma unroll
+          for (int h = 0; h < kHold / 32; ++h)
+            if (32 * h < valid) {   // warp-uniform
+              if constexpr (kBN == 128) {
+                tc_ld_32_bf16<!kMx>(tcol + 32u * h, scale, hb + 16 * h);
+              } else {
+                tc_ld_16_bf16<!kMx>(tcol + 32u * h, scale, hb + 16 * h);
+                tc_ld_16_bf16<!kMx>(tcol + 32u * h + 16u, scale, hb + 16 * h + 8);
+              }
+            }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -1181,35 +1370,14 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
             else mbar_arrive(acce_bar(acc));
           }
           released = true;
-          __nv_bfloat16* Y = static_cast<__nv_bfloat16*>(p.Y);
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            if (16 * g < valid) {   // warp-uniform
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                const uint32_t w = hb[8 * g + j / 2];
-                asm volatile("st.shared.u16 [%0], %1;" ::"r"(obuf_s + (uint32_t)(j * 64 + lane * 2)),
-                             "h"((unsigned short)(w & 0xffffu)) : "memory");
-                asm volatile("st.shared.u16 [%0], %1;" ::"r"(obuf_s + (uint32_t)((j + 1) * 64 + lane * 2)),
-                             "h"((unsigned short)(w >> 16)) : "memory");
-              }
-              __syncwarp();
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {   // 16 tokens x 4 chunks of 16 B
-                const int ci = lane + 32 * k, tok = ci >> 2, part = ci & 3;
-                if (16 * g + tok < valid) {
-                  uint32_t a, b, cc, d;
-                  lds128(obuf_s + (uint32_t)(tok * 64 + part * 16), a, b, cc, d);
-                  *reinterpret_cast<uint4*>(Y + (size_t)(r0 + 16 * g + tok) * p.N + col0 + part * 8) =
-                      make_uint4(a, b, cc, d);
-                }
-              }
-              __syncwarp();
-            }
-          }
+          for (int g = 0; g < kHold / 32; ++g)
+            if (32 * g < valid) store32(32 * g, hb + 16 * g);   // warp-uniform
         }
       }
-      for (int u = u_begin; u < u_end && !released; ++u) {
+      const bool direct = kBN >= 128 && G::kNT == 1 + (kWide ? 1 : 0) && !p.y_f32 && p.perm_src == nullptr;
+      for (int u = u_begin; u < u_end && !direct; ++u) {
+
       // first feature of this warp
       const size_t col0 = ((size_t)c.nt * kCG * G::kNT + u * kCG + rank) * kTileN + 32 * q;
       for (int c0 = 0; c0 < valid; c0 += 16) {
@@ -1318,12 +1486,14 @@ static GemmPlan make_plan(int fmt, int BN, int E, int tcap, bool glu = false, in
   const int nt = glu || wide ? 2 : 1;
   g.cps = stage_chunks(fmt, BN, glu, cg, wide);
   const int sfps = g.cps * fmt_sf_chunk(fmt);
-  const int body = g.cps * (BN / cg) * fmt_act_chunk(fmt) + nt * g.cps * fmt_w_chunk(fmt) + sfps * 512;
+  const int body = g.cps * (BN / cg) * 128 + nt * g.cps * fmt_w_chunk(fmt) + (fmt_mx(fmt) ? 0 : sfps * 512);
   g.stage = (body + 1023) / 1024 * 1024;
   // everything but the stage ring and the tile table, at its largest
   const int ostage = (wide ? 8 : 4) * (glu ? kGluStageBytes : kOutStageBytes);
+  // the microscaled formats' scale ring and its barriers
+  const int sring = fmt_mx(fmt) ? kScaleRing * ((nt + sfb_atoms(BN)) * sfps * 512 + 16) : 0;
   const int fixed = 1024 + (2 * kMaxStages + kNSets + 2 * kMaxAcc + 2) * 8 + (int)sizeof(Ctl) + (3 * E + 2) * 4 +
-                    16 + (E + 1) * 8 + 16 + ostage;
+                    16 + (E + 1) * 8 + 16 + ostage + sring;
   int budget = g_smem_limit - fixed;
   if (BN == 128 && cg == 1 && budget > kStageBudget128) budget = kStageBudget128;
   g.stages = (budget - tcap * 16) / g.stage;
@@ -1337,12 +1507,12 @@ static GemmPlan make_plan(int fmt, int BN, int E, int tcap, bool glu = false, in
     g.tcap = (budget - ring * g.stage) / 16;
   }
   const int acc_stride = (BN < 32 ? 32 : BN) * nt;
-  g.nacc = (int)((kTmemCols - kColAcc) / acc_stride);
+  g.nacc = (int)((kTmemCols - col_acc(fmt)) / acc_stride);
   if (g.nacc > kMaxAcc) g.nacc = kMaxAcc;
   const int nbars = 2 * g.stages + kNSets + 2 * g.nacc + 2;
   g.smem = 1024 + (size_t)g.stages * g.stage + nbars * 8 + sizeof(Ctl) + (size_t)(3 * E + 2) * 4 + 16 +
            (size_t)(E + 1) * 8 + 16 +
-           (size_t)g.tcap * 16 + ostage;
+           (size_t)g.tcap * 16 + ostage + sring;
   return g;
 }
 
@@ -1364,6 +1534,35 @@ int gemm_pick_bn(int max_rows, int R, int E) {
   if (max_rows > 0 && max_rows <= 32) return 32;
   if (max_rows > 0 && max_rows <= 64) return 64;
   return (long long)R >= 64ll * E ? 128 : 64;
+}
+
+// Token tile of the microscaled formats.  Up to 32 rows in every expert: the smallest tile that holds them,
+// one CTA per tile.  Beyond: 64 tokens on one CTA, or 128 or 192 on a wide pair tile, whichever an estimate in
+// SM cycles makes cheaper for experts of R / E rows each (measured by SM clock, 1.9 GHz).  `chunks` ring
+// stages make a tile; a wide one takes max(620, 4 N) cycles for N tokens (4 N: the tensor pipe's time for
+// 512 x N x one chunk; 620: issuing it), its single accumulator buffer costs 1500 or 3400 more between tiles,
+// and the pair launch about 4000 at its ends; a 64-token stage takes 700 (470 with 8-bit activations, half as
+// long).  Measured, N = 4096, K = 7168, 4-bit, 64 / 128 / 192 tokens: 64 experts x 100 rows 298 / 162 / -,
+// x 171 rows - / 244 / 200, x 300 rows - / 382 / 296 us; one expert x 1023 rows 55 / 19.1 / 21.8 us, x 4096
+// rows - / 57 / 51 us; 8 experts x 100 rows, N = K = 1024: 7.1 / 13.4 / - us.
+static int mx_pick_bn(int max_rows, int R, int E, int N, int chunks, bool act8, int num_sms, int pairs) {
+  if (max_rows > 0 && max_rows <= 16) return 16;
+  if (max_rows > 0 && max_rows <= 32) return 32;
+  if (pairs == 0) return 64;
+  const int bns[3] = {64, 128, 192};
+  const long long rows = ((long long)R + E - 1) / E, nt = N / kTileN;
+  long long best = 0;
+  int bn = 64;
+  for (int i = 0; i < 3; ++i) {
+    const bool wide = bns[i] > 64;
+    const long long n = (rows + bns[i] - 1) / bns[i], units = wide ? pairs : num_sms;
+    const long long tokens = ((rows + n - 1) / n + 15) / 16 * 16;
+    const long long waves = (n * E * (wide ? (nt + 3) / 4 : nt) + units - 1) / units;
+    const long long stage = !wide ? (act8 ? 470 : 700) : 4 * tokens > 620 ? 4 * tokens : 620;
+    const long long cost = (wide ? 4000 : 0) + waves * (chunks * stage + (i == 0 ? 1000 : i == 1 ? 1500 : 3400));
+    if (i == 0 || cost < best) { best = cost; bn = bns[i]; }
+  }
+  return bn;
 }
 
 bool gemm_supported(int E) { return E >= 1 && E <= kMaxE; }
@@ -1399,7 +1598,7 @@ template <int kFmt, bool kWide = false>
 static int max_pairs(int smem) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(gemm_threads(kWide));
+  cfg.blockDim = dim3(gemm_threads(kFmt, kWide));
   cfg.dynamicSmemBytes = (size_t)smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1433,19 +1632,18 @@ cudaError_t gemm_set_smem_attrs() {
       set_attr_one<S, 128, false, 2>(maxb), set_attr_one<D, 128, false, 2>(maxb),
       set_attr_one<D, 128, false, 1, true>(maxb), set_attr_one<S, 128, false, 2, false, true>(maxb),
       set_attr_one<D, 128, false, 2, false, true>(maxb),
-      set_attr_one<M4, 16>(maxb), set_attr_one<M4, 32>(maxb), set_attr_one<M4, 64>(maxb), set_attr_one<M4, 128>(maxb),
+      set_attr_one<M4, 16>(maxb), set_attr_one<M4, 32>(maxb), set_attr_one<M4, 64>(maxb),
       set_attr_one<M8, 16>(maxb), set_attr_one<M8, 32>(maxb), set_attr_one<M8, 64>(maxb),
-      set_attr_one<M4, 128, false, 2>(maxb), set_attr_one<M8, 128, false, 2>(maxb),
-      set_attr_one<M4, 128, false, 2, false, true>(maxb)};
+      set_attr_one<M4, 128, false, 2, false, true>(maxb), set_attr_one<M8, 128, false, 2, false, true>(maxb),
+      set_attr_one<M4, 192, false, 2, false, true>(maxb), set_attr_one<M8, 192, false, 2, false, true>(maxb)};
   for (cudaError_t x : errs)
     if (x != cudaSuccess) return x;
   g_pair_units[S] = max_pairs<S>(maxb);
   g_pair_units[D] = max_pairs<D>(maxb);
-  g_pair_units[M4] = max_pairs<M4>(maxb);
-  g_pair_units[M8] = max_pairs<M8>(maxb);
   g_wide_units[S] = max_pairs<S, true>(maxb);
   g_wide_units[D] = max_pairs<D, true>(maxb);
-  g_wide_units[M4] = max_pairs<M4, true>(maxb);   // (8-bit activations: a wide stage leaves room for two only)
+  g_wide_units[M4] = max_pairs<M4, true>(maxb);
+  g_wide_units[M8] = max_pairs<M8, true>(maxb);
   return cudaSuccess;
 }
 
@@ -1454,9 +1652,9 @@ static cudaError_t launch_bn(int BN, int grid, size_t smem, cudaStream_t stream,
                              const CUtensorMap& tb64, const CUtensorMap& ts, const CUtensorMap& tw,
                              const GemmParams& p) {
   switch (BN) {
-    case 16: return launch_pdl(grouped_gemm_kernel<kFmt, 16, kGLU, 1>, grid, kGemmThreads, smem, stream, tb, tb64, ts, tw, p);
-    case 32: return launch_pdl(grouped_gemm_kernel<kFmt, 32, kGLU, 1>, grid, kGemmThreads, smem, stream, tb, tb64, ts, tw, p);
-    default: return launch_pdl(grouped_gemm_kernel<kFmt, 64, kGLU, 1>, grid, kGemmThreads, smem, stream, tb, tb64, ts, tw, p);
+    case 16: return launch_pdl(grouped_gemm_kernel<kFmt, 16, kGLU, 1>, grid, gemm_threads(kFmt, false), smem, stream, tb, tb64, ts, tw, p);
+    case 32: return launch_pdl(grouped_gemm_kernel<kFmt, 32, kGLU, 1>, grid, gemm_threads(kFmt, false), smem, stream, tb, tb64, ts, tw, p);
+    default: return launch_pdl(grouped_gemm_kernel<kFmt, 64, kGLU, 1>, grid, gemm_threads(kFmt, false), smem, stream, tb, tb64, ts, tw, p);
   }
 }
 
@@ -1468,19 +1666,23 @@ static cudaError_t launch_fmt(int BN, int grid, size_t smem, cudaStream_t stream
     if (glu) return launch_bn<kFmt, true>(BN, grid, smem, stream, tb, tb64, ts, tw, p);
   if constexpr (kFmt == kFmtDense)
     if (native)
-      return launch_pdl(grouped_gemm_kernel<kFmt, 128, false, 1, true>, grid, kGemmThreads, smem, stream, tb, tb64, ts,
+      return launch_pdl(grouped_gemm_kernel<kFmt, 128, false, 1, true>, grid, gemm_threads(kFmt, false), smem, stream, tb, tb64, ts,
                         tw, p);
-  if constexpr (kFmt != kFmtMx8)
-    if (BN == 128 && pair && wide)
-      return launch_pdl_cluster(grouped_gemm_kernel<kFmt, 128, false, 2, false, true>, grid, kGemmThreadsWide, smem,
+  if constexpr (fmt_mx(kFmt))
+    if (BN == 192)
+      return launch_pdl_cluster(grouped_gemm_kernel<kFmt, 192, false, 2, false, true>, grid, gemm_threads(kFmt, true), smem,
                                 stream, 2u, tb, tb64, ts, tw, p);
-  if (BN == 128 && pair)
-    return launch_pdl_cluster(grouped_gemm_kernel<kFmt, 128, false, 2>, grid, kGemmThreads, smem, stream, 2u, tb,
-                              tb64, ts, tw, p);
-  if constexpr (kFmt != kFmtMx8)
+  if (BN == 128 && pair && wide)
+    return launch_pdl_cluster(grouped_gemm_kernel<kFmt, 128, false, 2, false, true>, grid, gemm_threads(kFmt, true), smem,
+                              stream, 2u, tb, tb64, ts, tw, p);
+  if constexpr (!fmt_mx(kFmt)) {
+    if (BN == 128 && pair)
+      return launch_pdl_cluster(grouped_gemm_kernel<kFmt, 128, false, 2>, grid, gemm_threads(kFmt, false), smem, stream,
+                                2u, tb, tb64, ts, tw, p);
     if (BN == 128)
-      return launch_pdl(grouped_gemm_kernel<kFmt, 128, false, 1>, grid, kGemmThreads, smem, stream, tb, tb64, ts, tw,
-                        p);
+      return launch_pdl(grouped_gemm_kernel<kFmt, 128, false, 1>, grid, gemm_threads(kFmt, false), smem, stream, tb, tb64,
+                        ts, tw, p);
+  }
   return launch_bn<kFmt, false>(BN, grid, smem, stream, tb, tb64, ts, tw, p);
 }
 
@@ -1496,31 +1698,32 @@ int launch_gemm(int fmt, const uint8_t* a_codes, const uint8_t* a_scales, const 
   const bool glu = h_scales != nullptr;
   if (native && (fmt != kFmtDense || glu || comb != nullptr)) return 1;
   if ((glu || comb != nullptr) && fmt != kFmtSparse) return 1;
-  int BN = native ? 128 : gemm_pick_bn(max_rows, R, E);   // the native orientation: 128-token tiles (MMA M)
+  const int mx_pairs = g_wide_units[fmt] < num_sms / 2 ? g_wide_units[fmt] : num_sms / 2;
+  int BN = native        ? 128   // the native orientation: 128-token tiles (MMA M)
+           : fmt_mx(fmt) ? mx_pick_bn(max_rows, R, E, N, K / fmt_chunk_k(fmt), fmt == kFmtMx8, num_sms, mx_pairs)
+                         : gemm_pick_bn(max_rows, R, E);
   if (glu && BN > 64) BN = 64;   // two accumulators per tile: 64-token tiles at most
-  // 8-bit activations: 128-token tiles only on CTA pairs (one CTA's 66 KB stage leaves room for two, and
-  // the TMEM sets need three)
-  if (fmt == kFmtMx8 && BN == 128 && ((N / kTileN) % 2 != 0 || g_pair_units[fmt] == 0)) BN = 64;
   // 128-token tiles run as CTA pairs (256 weight rows per tile) when N holds whole n-tile pairs
   // and the device can co-schedule pairs
-  // a wide pair tile (no combine epilogue, N a multiple of 512) holds two n-tile pairs, 512 weight
-  // rows, and reads its 128 tokens' activations once for both
-  const bool wide = BN == 128 && !glu && !native && comb == nullptr && (N / kTileN) % 4 == 0 &&
+  // a wide pair tile (no combine epilogue, N a multiple of 512; the microscaled formats: any N) holds two
+  // n-tile pairs, 512 weight rows, and reads its tokens' activations once for both
+  const bool wide = BN >= 128 && !glu && !native && comb == nullptr && (fmt_mx(fmt) || (N / kTileN) % 4 == 0) &&
                     g_wide_units[fmt] > 0;
   const int pair_units = wide ? g_wide_units[fmt] : g_pair_units[fmt];
-  const bool pair = BN == 128 && !glu && !native && (N / kTileN) % 2 == 0 && pair_units > 0;
+  const bool pair = wide || (BN == 128 && !glu && !native && (N / kTileN) % 2 == 0 && pair_units > 0);
   const int cg = pair ? 2 : 1;
   const int units = pair ? (pair_units < num_sms / 2 ? pair_units : num_sms / 2) : num_sms;   // pairs or CTAs
   const int grid = units * cg;
   const int ntt = glu || (pair && wide) ? 2 : 1;   // weight n-tiles per tile and CTA
-  const long long bound = (((long long)R + BN - 1) / BN + E) * (N / kTileN / ntt / cg);
+  const int NTt = ceil_div_i(N / kTileN, ntt * cg);
+  const long long bound = (((long long)R + BN - 1) / BN + E) * NTt;
   // schedule: contiguous byte-balanced runs when every expert fits one token tile (max_rows known)
   // and the CTAs can hold at least 32 tiles each (at most min(E, R) experts are touched), else
   // round-robin
-  const int NTt = N / kTileN / ntt / cg;
   const long long touched_max = R < E ? R : E;
   const int sched = (!pair && max_rows > 0 && max_rows <= BN && touched_max * NTt >= 32LL * units) ? kSchedRuns
-                                                                                                  : kSchedRoundRobin;
+                    : fmt_mx(fmt) && BN >= 128                                                     ? kSchedRotate
+                                                                                                   : kSchedRoundRobin;
   long long tcap;
   if (sched == kSchedRuns) {
     // a CTA's share of the bytes holds at most (wc + BN ac) / (wc + ac) times the average tile count
@@ -1538,8 +1741,8 @@ int launch_gemm(int fmt, const uint8_t* a_codes, const uint8_t* a_scales, const 
   const int box_h = g.BN / cg < 32 ? g.BN / cg : 32;
   const int sfps = g.cps * fmt_sf_chunk(fmt);
   const int rcap = R + (fmt_mx(fmt) ? 0 : kActScalePadRows);   // (TMA boxes past the last row read zeros)
-  const int KBa = K / 256 * fmt_sf_chunk(fmt);
-  const cuuint64_t row_bytes = (cuuint64_t)(K / 256) * fmt_act_chunk(fmt);
+  const int KBa = K / fmt_chunk_k(fmt) * fmt_sf_chunk(fmt);
+  const cuuint64_t row_bytes = (cuuint64_t)(K / fmt_chunk_k(fmt)) * 128;
   CUtensorMap tb, tb64, ts, tw;
   // activation codes [R][K/2] ([R][K] for 8-bit activations): boxes of 128 bytes x box_h rows, and (token tiles >= 64) x 64 rows
   for (int m = 0; m < 2; ++m) {
@@ -1554,12 +1757,13 @@ int launch_gemm(int fmt, const uint8_t* a_codes, const uint8_t* a_scales, const 
       return 2;
   }
   {
-    // activation scale quad entries as a [KBa][rcap][16 B] tensor; one box = the stage's atoms
-    cuuint64_t dims[3] = {16u, (cuuint64_t)rcap, (cuuint64_t)KBa};
-    cuuint64_t strides[2] = {16u, (cuuint64_t)rcap * 16u};
-    cuuint32_t box[3] = {16u, 32u, (cuuint32_t)sfps};
-    cuuint32_t estr[3] = {1u, 1u, 1u};
-    if (enc(&ts, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(a_scales), dims, strides, box, estr,
+    // activation scale quad entries as a [KBa][rcap * 4] tensor of 32-bit words; one box = the stage's atoms
+    // (32 entries of 16 bytes are one row of a box)
+    cuuint64_t dims[2] = {(cuuint64_t)rcap * 4u, (cuuint64_t)KBa};
+    cuuint64_t strides[1] = {(cuuint64_t)rcap * 16u};
+    cuuint32_t box[2] = {128u, (cuuint32_t)sfps};
+    cuuint32_t estr[2] = {1u, 1u};
+    if (enc(&ts, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<uint8_t*>(a_scales), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return 2;
