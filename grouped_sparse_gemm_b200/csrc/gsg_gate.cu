@@ -277,7 +277,7 @@ moe_gate_kernel(const GateParams p) {
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (!group_open(p, kept, 32 * i + lane)) c[i] = neg_inf();
+        if (32 * i + lane < p.E && !group_open(p, kept, 32 * i + lane)) c[i] = neg_inf();
     }
     // At least k experts have the k-th largest of the 32 lanes' maxima or more; the chosen ones, and all
     // whose order with them is uncertain, are among those that come up to it less the margin.
