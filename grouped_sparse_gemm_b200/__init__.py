@@ -527,9 +527,7 @@ def _args(stream, *ts: Optional[torch.Tensor]) -> int:
     run) and the stream to launch on."""
     dev = torch.cuda.current_device()
     for t in ts:
-        if t is None:
-            continue
-        if t.get_device() != dev or not t.is_contiguous():
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
             if not t.is_cuda:
                 raise ValueError("grouped_sparse_gemm_b200 works on CUDA tensors only (no CPU fallback)")
             if t.get_device() != dev:
@@ -539,10 +537,12 @@ def _args(stream, *ts: Optional[torch.Tensor]) -> int:
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _out(t: Optional[torch.Tensor], shape, like: torch.Tensor, dtype, what: str) -> torch.Tensor:
-    """A new output on the device of `like`, or the caller's after a check of its shape and type."""
-    if t is None:
-        return like.new_empty(shape, dtype=dtype)
+def _new(rows: int, cols: int, dtype, device) -> torch.Tensor:
+    """A new [rows, cols] (with its strides given, a third cheaper to allocate than torch.empty)."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
+def _check_out(t: torch.Tensor, shape, dtype, what: str) -> torch.Tensor:
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} {dtype}")
     return t
@@ -556,12 +556,13 @@ def _mx_activations(out: Optional[MxActivations], R: int, K: int, fmt: int, like
     if fmt != MXFP4 and fmt != MXFP8:
         raise ValueError(f"fmt {fmt!r}: MXFP4 (4) or MXFP8 (8)")
     if out is None:
-        return MxActivations(like.new_empty((R, K * fmt // 8), dtype=torch.uint8),
-                             like.new_empty((K // 128 * R * 16,), dtype=torch.uint8), R, K, fmt)
+        dev = like.device
+        return MxActivations(_new(R, K * fmt // 8, torch.uint8, dev),
+                             torch.empty_strided((K // 128 * R * 16,), (1,), dtype=torch.uint8, device=dev), R, K, fmt)
     if (out.R, out.K, out.fmt) != (R, K, fmt):
         raise ValueError(f"out: R={out.R} K={out.K} fmt={out.fmt}, expected R={R} K={K} fmt={fmt}")
-    _out(out.codes, (R, K * fmt // 8), like, torch.uint8, "codes")
-    _out(out.scales, (K // 128 * R * 16,), like, torch.uint8, "scales")
+    _check_out(out.codes, (R, K * fmt // 8), torch.uint8, "codes")
+    _check_out(out.scales, (K // 128 * R * 16,), torch.uint8, "scales")
     return out
 
 
@@ -569,8 +570,10 @@ def _mx_weights(out: Optional[PackedMxWeights], E: int, N: int, K: int, like: to
     n = int(lib().gsg_mx_packed_bytes(E, N, K))
     if out is not None and (out.E, out.N, out.K) != (E, N, K):
         raise ValueError(f"out: E={out.E} N={out.N} K={out.K}, expected E={E} N={N} K={K}")
-    packed = _out(None if out is None else out.packed, (n,), like, torch.uint8, "packed")
-    return out if out is not None else PackedMxWeights(packed, E, N, K)
+    if out is None:
+        return PackedMxWeights(like.new_empty((n,), dtype=torch.uint8), E, N, K)
+    _check_out(out.packed, (n,), torch.uint8, "packed")
+    return out
 
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
@@ -589,8 +592,14 @@ def moe_gate(logits: torch.Tensor, top_k: int, scoring: str = "softmax", bias: O
     if bias is not None and (bias.dtype != torch.float32 or bias.numel() != E):
         raise ValueError(f"bias: fp32 of {E} entries wanted")
     s = _args(stream, logits, bias, out_ids, out_gates)
-    out_ids = _out(out_ids, (T, top_k), logits, torch.int32, "out_ids")
-    out_gates = _out(out_gates, (T, top_k), logits, torch.float32, "out_gates")
+    if out_ids is None:
+        out_ids = _new(T, top_k, torch.int32, logits.device)
+    else:
+        _check_out(out_ids, (T, top_k), torch.int32, "out_ids")
+    if out_gates is None:
+        out_gates = _new(T, top_k, torch.float32, logits.device)
+    else:
+        _check_out(out_gates, (T, top_k), torch.float32, "out_gates")
     _check("gsg_moe_gate", lib().gsg_moe_gate(
         logits.data_ptr(), OUT_F32 if logits.dtype == torch.float32 else OUT_BF16, _ptr_of(bias), T, E, top_k,
         _SCORES[scoring], n_group, topk_group, group_top, 1 if renormalize else 0, scale, out_ids.data_ptr(),
@@ -616,9 +625,9 @@ def add_rmsnorm_mx(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     if residual is not None:
         if residual.shape != x.shape or residual.dtype not in (torch.float32, torch.bfloat16):
             raise ValueError(f"residual: fp32 or bf16 {tuple(x.shape)} wanted")
-        h = _out(out_h, x.shape, x, residual.dtype, "out_h")
+        h = torch.empty_like(residual) if out_h is None else _check_out(out_h, x.shape, residual.dtype, "out_h")
     if want_y or out_y is not None:
-        y = _out(out_y, x.shape, x, torch.bfloat16, "out_y")
+        y = torch.empty_like(x) if out_y is None else _check_out(out_y, x.shape, torch.bfloat16, "out_y")
     if fmt is not None:
         act = _mx_activations(out_act, T, K, fmt, x)
     _check("gsg_add_rmsnorm_mx", lib().gsg_add_rmsnorm_mx(
@@ -691,7 +700,10 @@ def grouped_mx_gemm(act: MxActivations, w: PackedMxWeights, offsets: torch.Tenso
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"out: bf16 or fp32, got {out_dtype}")
     s = _args(stream, act.codes, act.scales, w.packed, offsets, out)
-    out = _out(out, (act.R, w.N), act.codes, out_dtype, "out")
+    if out is None:
+        out = _new(act.R, w.N, out_dtype, act.codes.device)
+    else:
+        _check_out(out, (act.R, w.N), out_dtype, "out")
     _check("gsg_grouped_mx_gemm", lib().gsg_grouped_mx_gemm(
         act.codes.data_ptr(), act.scales.data_ptr(), act.fmt, w.packed.data_ptr(), offsets.data_ptr(), w.E, w.N, w.K,
         act.R, max_rows_per_expert, out.data_ptr(), OUT_F32 if out_dtype == torch.float32 else OUT_BF16, s))
