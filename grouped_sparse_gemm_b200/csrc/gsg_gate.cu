@@ -33,8 +33,8 @@ struct GateParams {
 };
 
 constexpr int kGateWarps = 4;
-// blocks per SM (registers: 64, 128 and 168 a thread)
-constexpr int gate_blocks(int nv) { return nv <= 12 ? 8 : nv <= 16 ? 4 : 3; }
+// blocks per SM (registers: 64, 72, 128 and 168 a thread)
+constexpr int gate_blocks(int nv) { return nv <= 8 ? 8 : nv <= 12 ? 7 : nv <= 16 ? 4 : 3; }
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
 // Order-preserving unsigned key of a float (no NaN); -0 counts as +0.  Every key is above 0.
@@ -80,10 +80,20 @@ __device__ __forceinline__ float bias_of(const GateParams& p, int e) {
   return p.bias != nullptr ? __ldg(p.bias + e) : 0.0f;
 }
 
-// Scores in 32 bits; softmax: mx the row's largest logit, inv_sum 1 / its denominator.
-__device__ __forceinline__ float score_sigmoid(float x) { return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-x))); }
+// Scores in 32 bits; softmax: mx the row's largest logit, inv_sum 1 / its denominator.  Two hardware
+// approximations each (2^x and 1 / x, results below the normal range flushed): see order_margin.
+__device__ __forceinline__ float fast_exp(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fmul_rn(x, 1.44269504f)));
+  return r;
+}
+__device__ __forceinline__ float score_sigmoid(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, fast_exp(-x))));
+  return r;
+}
 __device__ __forceinline__ float score_softmax(float x, float mx, float inv_sum) {
-  return __fmul_rn(__expf(__fsub_rn(x, mx)), inv_sum);
+  return __fmul_rn(fast_exp(__fsub_rn(x, mx)), inv_sum);
 }
 // Is expert e in one of the kept groups?
 __device__ __forceinline__ bool group_open(const GateParams& p, uint32_t kept, int e) {
@@ -186,7 +196,8 @@ __global__ void __launch_bounds__(32 * kGateWarps, gate_blocks(NV))
 moe_gate_kernel(const GateParams p) {
   extern __shared__ float gate_sh[];   // with groups: the choices of each warp's token, [kGateWarps][E]
   __shared__ int cand_sh[kGateWarps][32];
-  __shared__ float2 rank_sh[kGateWarps][32];
+  __shared__ unsigned long long key_sh[kGateWarps][32];
+  __shared__ float sort_sh[kGateWarps][32];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -194,43 +205,46 @@ moe_gate_kernel(const GateParams p) {
   const int lpg = p.n_group > 16 ? 1 : p.n_group > 8 ? 2 : p.n_group > 4 ? 4 : p.n_group > 2 ? 8 : 16;
   float* sh = gate_sh + (size_t)warp * p.E;
   float b[NV];   // the biases; -inf: no such expert, or never available
+  uint32_t there = 0u;   // bit i: expert 32 i + lane exists
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = 32 * i + lane;
+    if (e < p.E) there |= 1u << i;
     b[i] = e < p.E ? bias_of(p, e) : neg_inf();
     if (!(b[i] < INFINITY)) { bad = true; b[i] = neg_inf(); }
   }
   for (int t = blockIdx.x * kGateWarps + warp; t < p.T; t += gridDim.x * kGateWarps) {
     const size_t row = (size_t)t * p.E;
-    float c[NV];   // the logits, then the choices
+    float c[NV];   // the logits, then the choices (experts that do not exist: the lowest number, until the bias)
     float probe = 0.0f, mx = neg_inf();
 #pragma unroll
-    for (int i = 0; i < NV; ++i) c[i] = 32 * i + lane < p.E ? load_logit<T>(p.logits, row + 32 * i + lane) : neg_inf();
-#pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (32 * i + lane < p.E) probe = __fmaf_rn(c[i], 0.0f, probe);
-      mx = fmaxf(mx, c[i]);
+      c[i] = -3.402823466e38f;
+      if ((there >> i) & 1u) c[i] = load_logit<T>(p.logits, row + 32 * i + lane);
     }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) probe = __fmaf_rn(c[i], 0.0f, probe);
     // bit i: expert 32 i + lane is unavailable by its logit (NaN and +inf are errors)
     uint32_t closed = 0u;
     if (__any_sync(0xffffffffu, probe != 0.0f)) {
-      mx = neg_inf();
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (!(c[i] < INFINITY)) { bad = true; c[i] = neg_inf(); }
+        if (!((there >> i) & 1u)) c[i] = neg_inf();
         if (c[i] == neg_inf()) closed |= 1u << i;
-        mx = fmaxf(mx, c[i]);
       }
     }
     float inv_sum = 0.0f;
     if (!p.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) mx = fmaxf(mx, c[i]);
       mx = warp_max(mx);
       // the denominator, where the scores (not only the chosen experts' ratios) are needed
       if ((p.by_score || !p.renorm) && mx > neg_inf()) {
         float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) s = __fadd_rn(s, __expf(__fsub_rn(c[i], mx)));
+        for (int i = 0; i < NV; ++i) s = __fadd_rn(s, fast_exp(__fsub_rn(c[i], mx)));
         inv_sum = __frcp_rn(warp_sum(s));
       }
     }
@@ -248,6 +262,9 @@ moe_gate_kernel(const GateParams p) {
         for (int i = 0; i < NV; ++i)
           if ((closed >> i) & 1u) c[i] = neg_inf();
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) c[i] = __fadd_rn(c[i], b[i]);   // (0 or -inf)
     }
     ExactChoice<T> exact = {p, row, (double)mx, 0.0};
     bool have_exact_sum = false;
@@ -295,7 +312,8 @@ moe_gate_kernel(const GateParams p) {
     const float lim = p.by_score ? __fsub_rn(kth, order_margin(tol, kth)) : kth;
     uint32_t mask = 0u;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) mask |= c[i] >= lim && 32 * i + lane < p.E ? 1u << i : 0u;
+    for (int i = 0; i < NV; ++i) mask |= c[i] >= lim ? 1u << i : 0u;
+    mask &= there;
     const int n = __reduce_add_sync(0xffffffffu, __popc(mask));
     int my_e = 0, rank = 32;      // this lane's chosen expert and its place among the k (>= k: none)
     float my_x = neg_inf();       // its logit; -inf: unavailable
@@ -317,21 +335,26 @@ moe_gate_kernel(const GateParams p) {
         if (my_x > neg_inf())
           v = !p.by_score ? my_x : __fadd_rn(p.sigmoid ? score_sigmoid(my_x) : score_softmax(my_x, mx, inv_sum), be);
       }
-      rank_sh[warp][lane] = make_float2(v, __int_as_float(my_e));
+      // its rank: how many of the others come first by value, then by index
+      const unsigned long long key = lane < n ? (unsigned long long)order_key(v) << 32 | (uint32_t)~my_e : 0ull;
+      key_sh[warp][lane] = key;
       __syncwarp();
-      const float margin = order_margin(tol, v);
-      bool near = false;
       rank = 0;
 #pragma unroll 4
-      for (int j = 0; j < n; ++j) {
-        const float2 o = rank_sh[warp][j];
-        const int oe = __float_as_int(o.y);
-        rank += (o.x > v || (o.x == v && oe < my_e)) ? 1 : 0;
-        near |= fabsf(__fsub_rn(o.x, v)) <= margin && oe != my_e;
-      }
-      if (p.by_score && __any_sync(0xffffffffu, near && lane < n && rank < p.k)) {
-        exact_sum();
-        rank = exact_rank(my_x > neg_inf() ? exact(my_e) : -(double)INFINITY, my_e, n);
+      for (int j = 0; j < n; ++j) rank += key_sh[warp][j] > key ? 1 : 0;
+      if (p.by_score) {
+        // in order, is each of the first k (and the next) further than the margin above the one after it?
+        if (lane < n) sort_sh[warp][rank] = v;
+        __syncwarp();
+        bool near = false;
+        if (lane < p.k && lane + 1 < n) {
+          const float hi = sort_sh[warp][lane], lo = sort_sh[warp][lane + 1];
+          near = __fsub_rn(hi, lo) <= order_margin(tol, fmaxf(fabsf(hi), fabsf(lo)));
+        }
+        if (__any_sync(0xffffffffu, near)) {
+          exact_sum();
+          rank = exact_rank(my_x > neg_inf() ? exact(my_e) : -(double)INFINITY, my_e, n);
+        }
       }
       if (lane >= n) rank = 32;
       __syncwarp();   // the candidates are read before the next token's are written
@@ -398,15 +421,19 @@ moe_gate_kernel(const GateParams p) {
     // exp(x - max of the chosen) for softmax; for the sigmoid exp(x - m) / (1 + exp(x)), m = min(0, that max),
     // which keeps scores that would underflow apart.
     const bool chosen = rank < p.k;
-    const float mc = warp_max(chosen ? my_x : neg_inf());
     float g = 0.0f;
-    if (chosen && my_x > neg_inf()) {
-      if (p.sigmoid) {
-        const float off = p.renorm ? fminf(mc, 0.0f) : 0.0f;
-        g = my_x > 0.0f ? __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-my_x)))
-                        : __fdiv_rn(expf(__fsub_rn(my_x, off)), __fadd_rn(1.0f, expf(my_x)));
-      } else {
-        g = p.renorm ? expf(__fsub_rn(my_x, mc)) : __fmul_rn(expf(__fsub_rn(my_x, mx)), inv_sum);
+    if (p.sigmoid) {
+      float off = 0.0f;
+      if (p.renorm && !__any_sync(0xffffffffu, chosen && my_x >= 0.0f)) off = warp_max(chosen ? my_x : neg_inf());
+      const float q = expf(-fabsf(my_x));
+      float num = my_x > 0.0f ? 1.0f : q;
+      if (off != 0.0f) num = expf(__fsub_rn(my_x, off));
+      if (chosen && my_x > neg_inf()) g = __fdiv_rn(num, __fadd_rn(1.0f, q));
+    } else {
+      const float top = p.renorm ? warp_max(chosen ? my_x : neg_inf()) : mx;
+      if (chosen && my_x > neg_inf()) {
+        g = expf(__fsub_rn(my_x, top));
+        if (!p.renorm) g = __fmul_rn(g, inv_sum);
       }
     }
     if (p.renorm) {
