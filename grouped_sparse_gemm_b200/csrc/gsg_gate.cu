@@ -76,6 +76,24 @@ __device__ __forceinline__ float load_logit<uint16_t>(const void* p, size_t i) {
   return bf16_bits_to_f32(__ldg(static_cast<const uint16_t*>(p) + i));
 }
 
+// The same where lane < left, else the lowest number (a predicated load: a branch costs several times more).
+template <typename T>
+__device__ __forceinline__ float load_logit_if(const T* p, int lane, int left);
+template <>
+__device__ __forceinline__ float load_logit_if<float>(const float* p, int lane, int left) {
+  float v;
+  asm("{\n\t.reg .pred q;\n\tsetp.lt.s32 q, %2, %3;\n\tmov.b32 %0, 0xFF7FFFFF;\n\t@q ld.global.nc.f32 %0, [%1];\n\t}"
+      : "=f"(v) : "l"(p), "r"(lane), "r"(left));
+  return v;
+}
+template <>
+__device__ __forceinline__ float load_logit_if<uint16_t>(const uint16_t* p, int lane, int left) {
+  uint16_t v;
+  asm("{\n\t.reg .pred q;\n\tsetp.lt.s32 q, %2, %3;\n\tmov.b16 %0, 0xFF7F;\n\t@q ld.global.nc.u16 %0, [%1];\n\t}"
+      : "=h"(v) : "l"(p), "r"(lane), "r"(left));
+  return bf16_bits_to_f32(v);
+}
+
 __device__ __forceinline__ float bias_of(const GateParams& p, int e) {
   return p.bias != nullptr ? __ldg(p.bias + e) : 0.0f;
 }
@@ -201,7 +219,6 @@ moe_gate_kernel(const GateParams p) {
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t below = (1u << lane) - 1u;
   const int lpg = p.n_group > 16 ? 1 : p.n_group > 8 ? 2 : p.n_group > 4 ? 4 : p.n_group > 2 ? 8 : 16;
   float* sh = gate_sh + (size_t)warp * p.E;
   float b[NV];   // the biases; -inf: no such expert, or never available
@@ -219,10 +236,8 @@ moe_gate_kernel(const GateParams p) {
     float c[NV];   // the logits, then the choices (experts that do not exist: the lowest number, until the bias)
     float probe = 0.0f, mx = neg_inf();
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      c[i] = -3.402823466e38f;
-      if ((there >> i) & 1u) c[i] = load_logit<T>(p.logits, row + 32 * i + lane);
-    }
+    for (int i = 0; i < NV; ++i)
+      c[i] = load_logit_if<T>(static_cast<const T*>(p.logits) + row + lane + 32 * i, lane, p.E - 32 * i);
 #pragma unroll
     for (int i = 0; i < NV; ++i) probe = __fmaf_rn(c[i], 0.0f, probe);
     // bit i: expert 32 i + lane is unavailable by its logit (NaN and +inf are errors)
@@ -314,17 +329,18 @@ moe_gate_kernel(const GateParams p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) mask |= c[i] >= lim ? 1u << i : 0u;
     mask &= there;
-    const int n = __reduce_add_sync(0xffffffffu, __popc(mask));
+    int end = __popc(mask);       // candidates in this lane and those before it
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += v;
+    }
+    const int n = __shfl_sync(0xffffffffu, end, 31);
     int my_e = 0, rank = 32;      // this lane's chosen expert and its place among the k (>= k: none)
     float my_x = neg_inf();       // its logit; -inf: unavailable
     if (n <= 32) {
       // one candidate per lane
-      int base = 0;
-      for (uint32_t live; (live = __ballot_sync(0xffffffffu, mask != 0u)) != 0u; base += __popc(live))
-        if (mask != 0u) {
-          cand_sh[warp][base + __popc(live & below)] = 32 * (__ffs(mask) - 1) + lane;
-          mask &= mask - 1u;
-        }
+      for (; mask != 0u; mask &= mask - 1u) cand_sh[warp][--end] = 32 * (__ffs(mask) - 1) + lane;
       __syncwarp();
       float v = neg_inf();
       if (lane < n) {
@@ -340,8 +356,10 @@ moe_gate_kernel(const GateParams p) {
       key_sh[warp][lane] = key;
       __syncwarp();
       rank = 0;
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) rank += key_sh[warp][j] > key ? 1 : 0;
+      // (twelve at once, the usual number at most; keys past the last candidate are 0)
+#pragma unroll
+      for (int j = 0; j < 12; ++j) rank += key_sh[warp][j] > key ? 1 : 0;
+      for (int j = 12; j < n; ++j) rank += key_sh[warp][j] > key ? 1 : 0;
       if (p.by_score) {
         // in order, is each of the first k (and the next) further than the margin above the one after it?
         if (lane < n) sort_sh[warp][rank] = v;
@@ -438,7 +456,7 @@ moe_gate_kernel(const GateParams p) {
     }
     if (p.renorm) {
       const float sum = warp_sum(g);
-      g = sum > 0.0f ? __fdiv_rn(g, sum) : 0.0f;
+      if (g > 0.0f) g = __fdiv_rn(g, sum);   // (elsewhere 0; a division of 0 would take its slow path)
     }
     if (chosen) {
       p.ids[(size_t)t * p.k + rank] = my_e;
