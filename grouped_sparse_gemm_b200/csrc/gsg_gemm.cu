@@ -346,14 +346,20 @@ __device__ __forceinline__ void tc_ld_16(uint32_t taddr, float v[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// The same for 16 columns (fewer registers in flight).
-template <bool kScaled>
-__device__ __forceinline__ void tc_ld_16_bf16(uint32_t taddr, float scale, uint32_t h[8]) {
-  float v[16];
-  tc_ld_16(taddr, v);
+// Stores kPairs * 2 tokens of a warp's 32 features, h[i] this lane's feature of tokens 2i (low half) and 2i + 1:
+// neighbouring lanes trade halves, so that each holds two features of one token, and every store instruction
+// writes 64 whole bytes of two tokens' rows.  (Through shared memory, in 16-byte stores, it took twice the
+// load/store unit's time: 750 cycles for 32 tokens of a wide pair tile's eight epilogue warps.)
+// dst: this lane's place, token (lane & 1), features (lane & ~1) and the next; left: valid tokens from the first.
+template <int kPairs>
+__device__ __forceinline__ void store_pairs(__nv_bfloat16* dst, size_t ld, int left, int lane, const uint32_t* h) {
+  const uint32_t sel = (lane & 1) ? 0x3276 : 0x5410;
+  left -= lane & 1;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    h[i] = pack_bf16<kScaled>(v[2 * i], v[2 * i + 1], scale);
+  for (int i = 0; i < kPairs; ++i) {
+    const uint32_t w = __byte_perm(h[i], __shfl_xor_sync(0xffffffffu, h[i], 1), sel);
+    if (2 * i < left) *reinterpret_cast<uint32_t*>(dst) = w;
+    dst += 2 * ld;
   }
 }
 
@@ -1293,10 +1299,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
           // before any store, so the MMA warp's next tile waits for the loads, not for the stores
           const uint32_t tcol = taddr + (uint32_t)(u_begin * G::kAccStride);
           const int col0 = (c.nt * kCG * G::kNT + u_begin * kCG + (int)rank) * kTileN + 32 * q;
-          // tokens t0 .. t0 + 31 of the tile, h16[i] this lane's feature of tokens t0 + 2i (low half) and
-          // t0 + 2i + 1: neighbouring lanes trade halves, so that each holds two features of one token, and
-          // the block crosses the warp's buffer as [token][feature] in 32-bit words (conflict-free)
-          // (NVFP4, whose extra scaling leaves fewer registers: sixteen tokens at a time, a half word each)
+          // tokens t0 .. t0 + 31 of the tile, h16[i] this lane's feature of tokens t0 + 2i (low half) and t0 + 2i + 1
+          // (NVFP4, whose extra scaling leaves fewer registers: through the warp's buffer, sixteen tokens at a time)
           auto store32 = [&](int t0, const uint32_t* h16) {
             if constexpr (!kMx) {
 #pragma unroll
@@ -1326,43 +1330,22 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
               }
               return;
             }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint32_t other = __shfl_xor_sync(0xffffffffu, h16[i], 1);
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(obuf_s + (uint32_t)((2 * i + (lane & 1)) * 64 + (lane >> 1) * 4)),
-                           "r"(__byte_perm(h16[i], other, (lane & 1) ? 0x3276 : 0x5410)) : "memory");
-            }
-            __syncwarp();
-            __nv_bfloat16* Yl = static_cast<__nv_bfloat16*>(p.Y) + (size_t)(r0 + t0 + (lane >> 2)) * p.N + col0 + (lane & 3) * 8;
-#pragma unroll 2
-            for (int k = 0; k < 4; ++k) {   // 32 tokens x 4 chunks of 16 B
-              uint32_t a, b, cc, d;
-              lds128(obuf_s + (uint32_t)(k * 512 + lane * 16), a, b, cc, d);
-              if (t0 + 8 * k + (lane >> 2) < valid)
-                *reinterpret_cast<uint4*>(Yl + (size_t)(8 * k) * p.N) = make_uint4(a, b, cc, d);
-            }
-            __syncwarp();
+            store_pairs<16>(static_cast<__nv_bfloat16*>(p.Y) + (size_t)(r0 + t0 + (lane & 1)) * p.N + col0 + (lane & ~1),
+                            (size_t)p.N, valid - t0, lane, h16);
           };
-          constexpr int kHold = kBN < 160 ? kBN : 160;   // (what a thread's 128 registers hold without spills)
-          if constexpr (kHold < kBN) {
-            static_assert(kBN - kHold == 32, "one block of 32 tokens before the rest");
-            if (kHold < valid) {
+          // (128 tokens are what a thread's registers hold; a 192-token tile's others are stored first)
+          if constexpr (kBN > 128) {
+#pragma unroll 1
+            for (int t0 = 128; t0 < valid; t0 += 32) {
               uint32_t h16[16];
-              tc_ld_32_bf16<!kMx>(tcol + kHold, scale, h16);
-              store32(kHold, h16);
+              tc_ld_32_bf16<!kMx>(tcol + t0, scale, h16);
+              store32(t0, h16);
             }
           }
-          uint32_t hb[kHold / 2];
+          uint32_t hb[64];
 #pragma unroll
-          for (int h = 0; h < kHold / 32; ++h)
-            if (32 * h < valid) {   // warp-uniform
-              if constexpr (kBN == 128) {
-                tc_ld_32_bf16<!kMx>(tcol + 32u * h, scale, hb + 16 * h);
-              } else {
-                tc_ld_16_bf16<!kMx>(tcol + 32u * h, scale, hb + 16 * h);
-                tc_ld_16_bf16<!kMx>(tcol + 32u * h + 16u, scale, hb + 16 * h + 8);
-              }
-            }
+          for (int h = 0; h < 4; ++h)
+            if (32 * h < valid) tc_ld_32_bf16<!kMx>(tcol + 32u * h, scale, hb + 16 * h);   // warp-uniform
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -1371,7 +1354,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
           }
           released = true;
 #pragma unroll
-          for (int g = 0; g < kHold / 32; ++g)
+          for (int g = 0; g < 4; ++g)
             if (32 * g < valid) store32(32 * g, hb + 16 * g);   // warp-uniform
         }
       }
@@ -1398,6 +1381,12 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
               *reinterpret_cast<uint4*>(Y + (size_t)(r0 + c0 + tok) * p.N + col0 + part * 4) = make_uint4(a, b, cc, d);
             }
           }
+        } else if constexpr (kMx) {
+          uint32_t h8[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h8[j] = pack_bf16<false>(v[2 * j], v[2 * j + 1], 1.0f);
+          store_pairs<8>(static_cast<__nv_bfloat16*>(p.Y) + (size_t)(r0 + c0 + (lane & 1)) * p.N + col0 + (lane & ~1),
+                         (size_t)p.N, valid - c0, lane, h8);
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
