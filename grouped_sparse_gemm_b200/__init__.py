@@ -678,7 +678,7 @@ def quantize_act_mx(X: torch.Tensor, fmt: int = MXFP8, inv_perm: Optional[torch.
     s = _args(stream, X, inv_perm, workspace, None if out is None else out.codes, None if out is None else out.scales)
     out = _mx_activations(out, T * top_k, K, fmt, X)
     L = lib()
-    if workspace is None and T * top_k * K >= 1 << 27:   # (below that the call needs none)
+    if workspace is None and T * top_k * K >= 1 << 26:   # (below that the call needs none)
         workspace = _workspace(L.gsg_workspace_size(OP_QUANTIZE_MX, 0, 0, K, T, top_k), X.device)
     _check("gsg_quantize_act_mx", L.gsg_quantize_act_mx(
         X.data_ptr(), T, K, fmt, _ptr_of(inv_perm), top_k, out.codes.data_ptr(), out.scales.data_ptr(),

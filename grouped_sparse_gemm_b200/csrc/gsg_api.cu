@@ -107,7 +107,7 @@ size_t gsg_workspace_size(int op, int E, int N, int K, int T, int k) {
              gsg::quant_raw_bytes((long long)T * k, K);
     case GSG_OP_QUANTIZE_MX:   // (large R*K) the raw scale words
       if (T < 0 || K < 1 || k < 1) return 0;
-      return gsg::quant_raw_bytes((long long)T * k, K);
+      return gsg::quant_mx_raw_bytes((long long)T * k, K, k);
     case GSG_OP_COMBINE:   // slots bf16 [T*k][N], then counters int32 [T][N/32]
       if (T < 0 || k < 1 || N < 32) return 0;
       return combine_slot_bytes(T, k, N) + (size_t)T * (N / 32) * sizeof(int);

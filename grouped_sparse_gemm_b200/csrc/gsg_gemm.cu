@@ -285,25 +285,44 @@ __device__ __forceinline__ void tc_mma_dense_pair(uint32_t d, uint64_t adesc, ui
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
       : "memory");
 }
-// Microscaled forms (dense, one UE8M0 scale per 32 values): 4-bit weights against 4-bit (kM8 false)
-// or 8-bit activations, for one CTA or a CTA pair.  idesc names the bytes of the scale words used.
-template <bool kM8, bool kPair>
-__device__ __forceinline__ void tc_mma_mx(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate, uint32_t sfa, uint32_t sfb) {
-#define GSG_MX_MMA(CG, KIND)                                                                                   \
-  asm volatile(                                                                                                \
-      "{\n\t.reg .pred p, P;\n\t"                                                                              \
-      "setp.ne.b32 p, %4, 0;\n\t" GSG_ELECT                                                                    \
-      "@P tcgen05.mma.cta_group::" CG ".kind::" KIND ".block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d), \
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)                                  \
+// Descriptor bits for the byte of the 32-bit scale words (one byte per 32 values of a 128-wide k-block)
+// that an MMA's first 32 values use, in both operands.
+__host__ __device__ constexpr uint32_t idesc_sf(int sf) { return ((uint32_t)sf << 4) | ((uint32_t)sf << 29); }
+
+// The four MMAs of a microscaled chunk (dense, one UE8M0 scale per 32 values): 4-bit weights against 4-bit
+// (kM8 false, K = 64 each) or 8-bit activations (K = 32), for one CTA or a CTA pair.  Each takes the next 32 bytes of the operands' rows; idesc names the bytes of the scale words used
+// (see idesc_sf): with 8-bit activations one word holds all four MMAs' scales, else two words (four columns
+// each, kSfbStep for the tokens') two each.  `accumulate` is for the first of them.  (One election for the four:
+// a stage's issue bounds short tiles; 30B down-projection decode, 8-bit, 26.8 -> 25.8 us.  A predicate from a
+// register in place of elect.sync: 33.6 us.)
+template <bool kM8, bool kPair, int kSfbStep>
+__device__ __forceinline__ void tc_mma_mx_chunk(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t accumulate, uint32_t sfa, uint32_t sfb) {
+#define GSG_MX_MMA(CG, KIND, A, B, I, SA, SB, ACC) \
+  "@P tcgen05.mma.cta_group::" CG ".kind::" KIND ".block_scale.block32 [%0], " A ", " B ", " I ", [" SA "], [" SB "], " ACC ";\n\t"
+#define GSG_MX_CHUNK(CG, KIND, S1, S2, S3)                                                              \
+  asm volatile(                                                                                         \
+      "{\n\t.reg .pred P, p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t.reg .b32 i1, i2, i3, sa, sb;\n\t" \
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"                       \
+      "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"                               \
+      "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"                               \
+      "or.b32 i1, %3, %7;\n\tor.b32 i2, %3, %8;\n\tor.b32 i3, %3, %9;\n\t"                              \
+      "add.s32 sa, %5, %10;\n\tadd.s32 sb, %6, %11;\n\t" GSG_ELECT                                                \
+      GSG_MX_MMA(CG, KIND, "%1", "%2", "%3", "%5", "%6", "p")                                           \
+      GSG_MX_MMA(CG, KIND, "a1", "b1", "i1", "%5", "%6", "q")                                           \
+      GSG_MX_MMA(CG, KIND, "a2", "b2", "i2", "sa", "sb", "q")                                           \
+      GSG_MX_MMA(CG, KIND, "a3", "b3", "i3", "sa", "sb", "q") "}" ::                            \
+      "r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "n"(idesc_sf(S1)), \
+      "n"(idesc_sf(S2)), "n"(idesc_sf(S3)), "n"(kM8 ? 0 : 4), "n"(kM8 ? 0 : kSfbStep)                   \
       : "memory")
   if constexpr (kM8) {
-    if constexpr (kPair) GSG_MX_MMA("2", "mxf8f6f4");
-    else GSG_MX_MMA("1", "mxf8f6f4");
+    if constexpr (kPair) GSG_MX_CHUNK("2", "mxf8f6f4", 1, 2, 3);
+    else GSG_MX_CHUNK("1", "mxf8f6f4", 1, 2, 3);
   } else {
-    if constexpr (kPair) GSG_MX_MMA("2", "mxf4");
-    else GSG_MX_MMA("1", "mxf4");
+    if constexpr (kPair) GSG_MX_CHUNK("2", "mxf4", 2, 0, 2);
+    else GSG_MX_CHUNK("1", "mxf4", 2, 0, 2);
   }
+#undef GSG_MX_CHUNK
 #undef GSG_MX_MMA
 }
 // Two accumulators times `scale` (the microscaled formats have none), rounded to bf16, lo in the low half.
@@ -384,10 +403,6 @@ __host__ __device__ inline uint32_t make_idesc_mx(bool act8, int BN, int M) {
   return (act8 ? (5u << 7) : (1u << 7) | (1u << 10)) | ((uint32_t)(BN >> 3) << 17) | (1u << 23) |
          ((uint32_t)(M >> 4) << 24);
 }
-// Descriptor bits for the byte of the 32-bit scale words (one byte per 32 values of a 128-wide k-block)
-// that an MMA's first 32 values use, in both operands.
-__host__ __device__ constexpr uint32_t idesc_sf(int sf) { return ((uint32_t)sf << 4) | ((uint32_t)sf << 29); }
-
 struct Ctl {
   int abort;
   uint32_t tmem_base;
@@ -571,8 +586,6 @@ struct Geo {
   static constexpr int kCK = fmt_chunk_k(kFmt);                    // K values of a chunk
   static constexpr int kKbPerChunk = kCK / kKbLogical;             // MMAs per chunk: 2 sparse, else 4
   static constexpr int kSfPerChunk = fmt_sf_chunk(kFmt);           // scale atoms per chunk
-  static constexpr int kMmaPerSf = kKbPerChunk / kSfPerChunk;      // MMAs that share an atom (1 for NVFP4)
-  static constexpr int kSfIdStep = 4 / kMmaPerSf;                  // scale bytes each of them uses
   static constexpr int kCPS = stage_chunks(kFmt, kBN, kGLU, kCG, kWide);
   static constexpr int kSfps = kCPS * kSfPerChunk;                 // scale atoms per stage
   static constexpr int kCB = fmt_w_chunk(kFmt);                    // weight chunk block in shared memory
@@ -597,11 +610,6 @@ struct Geo {
   static constexpr int kAccStride = kBN < 32 ? 32 : kBN;
   static_assert(kSetUsed <= (int)kSetCols, "TMEM set too small");
   static_assert(kColAcc + kNT * kAccStride <= kTmemCols, "TMEM too small for one accumulator buffer");
-  // Operand A / B shared-memory descriptors' offsets of MMA h of a chunk: the NVFP4 weights are stored
-  // as the MMA's core matrices, 4096 bytes per MMA; the microscaled weights and all tokens are 128-byte
-  // swizzled rows, of which an MMA takes kBStep bytes.
-  __device__ static constexpr uint32_t a_off(int h) { return kMx ? 32u * h : 4096u * h; }
-  __device__ static constexpr uint32_t b_off(int h) { return kBStep * h; }
 };
 
 // kCG = 2: launched as clusters of two CTAs (a CTA pair on two SMs) that run 256-row weight tiles
@@ -1127,26 +1135,36 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
         tc_fence_after();
         const uint32_t st = sbase + (uint32_t)s * G::kStage;
         const uint32_t tset = tmem + (uint32_t)set * G::kSetCols;
+        if constexpr (kMx) {
+#pragma unroll
+          for (int ch = 0; ch < G::kCPS; ++ch)
+            if (ch < nch) {
+#pragma unroll
+              for (int t = 0; t < G::kNT; ++t)
+                tc_mma_mx_chunk<kFmt == kFmtMx8, kPair, 4 * G::kSfbA>(
+                    d_tmem + (uint32_t)(t * G::kAccStride),
+                    smem_desc(st + G::kOffW + (t * G::kCPS + ch) * G::kCB, 16, 1024, 2),
+                    smem_desc(st + ch * G::kBChunk, 16, 1024, 2), idesc, (kc | ch) != 0 ? 1u : 0u,
+                    tset + G::kColSFA + 4 * (t * G::kSfps + ch * G::kSfPerChunk),
+                    tset + G::kColSFB + 4 * G::kSfbA * ch * G::kSfPerChunk);
+            }
+        } else {
 #pragma unroll
         for (int ch = 0; ch < G::kCPS; ++ch) {
           if (ch < nch) {
 #pragma unroll
             for (int h = 0; h < G::kKbPerChunk; ++h) {
-              const int kbi = ch * G::kSfPerChunk + h / G::kMmaPerSf;   // scale atom
-              const uint64_t bdesc = smem_desc(st + ch * G::kBChunk + G::b_off(h), 16, 1024, 2);
+              const int kbi = ch * G::kSfPerChunk + h;   // scale atom
+              const uint64_t bdesc = smem_desc(st + ch * G::kBChunk + G::kBStep * h, 16, 1024, 2);
               const uint32_t accum = (kc | ch | h) != 0 ? 1u : 0u;
 #pragma unroll
               for (int t = 0; t < G::kNT; ++t) {
-                const uint32_t aaddr = st + G::kOffW + (t * G::kCPS + ch) * G::kCB + G::a_off(h);
-                const uint64_t adesc = kMx ? smem_desc(aaddr, 16, 1024, 2) : smem_desc(aaddr, 128, 256, 0);
+                const uint32_t aaddr = st + G::kOffW + (t * G::kCPS + ch) * G::kCB + 4096u * h;
+                const uint64_t adesc = smem_desc(aaddr, 128, 256, 0);
                 const uint32_t d = d_tmem + (uint32_t)(t * G::kAccStride);
                 const int kt = t * G::kSfps + kbi;
-                const uint32_t sfa = tset + G::kColSFA + 4 * kt, sfb = tset + G::kColSFB + 4 * G::kSfbA * kbi;
-                if constexpr (kMx)
-                  tc_mma_mx<kFmt == kFmtMx8, kPair>(
-                      d, adesc, bdesc, idesc | idesc_sf((h % G::kMmaPerSf) * G::kSfIdStep),
-                      accum, sfa, sfb);
-                else if constexpr (kNative)   // tokens as A, weights as B: the operands and their scales swap
+                const uint32_t sfa = tset + G::kColSFA + 4 * kt, sfb = tset + G::kColSFB + 4 * kbi;
+                if constexpr (kNative)   // tokens as A, weights as B: the operands and their scales swap
                   tc_mma_dense(d, bdesc, adesc, idesc, accum, sfb, sfa);
                 else if constexpr (kSparse && kPair)
                   tc_mma_sparse_pair(d, adesc, bdesc, idesc, accum, sfa, sfb, tset + 2 * kt);
@@ -1159,6 +1177,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
               }
             }
           }
+        }
         }
         if constexpr (kPair) tc_commit_pair(empty_bar(s), 3);   // the stage is free in both CTAs
         else tc_commit(empty_bar(s));

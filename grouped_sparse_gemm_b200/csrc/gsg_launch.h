@@ -39,7 +39,8 @@ cudaError_t launch_pack_mxfp4(const void* W, bool w_f32, int E, int N, int K, ui
 cudaError_t launch_pack_mxfp4_codes(const uint8_t* codes, const uint8_t* scales, int E, int N, int K, uint8_t* packed,
                                     int* status, cudaStream_t stream);
 cudaError_t quant_mx_set_smem_attrs();
-// bits: 4 or 8; raw: workspace of quant_raw_bytes(T*k, K) bytes for the two-phase scale path (nullptr: direct)
+size_t quant_mx_raw_bytes(long long R, int K, int k);
+// bits: 4 or 8; raw: workspace of quant_mx_raw_bytes(T*k, K, k) bytes for the two-launch scale path (nullptr: direct)
 cudaError_t launch_quant_mx(const uint16_t* X, int T, int K, int bits, const int32_t* inv_perm, int k, uint8_t* codes,
                             uint8_t* scales, uint32_t* raw, int* status, int num_sms, cudaStream_t stream);
 

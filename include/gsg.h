@@ -323,7 +323,7 @@ gsg_status_t gsg_pack_mxfp4_codes(const uint8_t* codes, const uint8_t* scales, i
  * Non-finite X sets GSG_ERR_NONFINITE, a routed row outside [0, R) GSG_ERR_BAD_ROUTING.  K % 256 == 0,
  * T*k <= 2^30, T*K/16 < 2^31, else GSG_ERR_UNSUPPORTED_SHAPE.
  * workspace: gsg_workspace_size(GSG_OP_QUANTIZE_MX, 0, 0, K, T, k) bytes, 16-byte aligned (0 below
- * R*K = 2^27: then it may be NULL). */
+ * R*K = 2^26, with k = 1 below 2^27: then it may be NULL). */
 gsg_status_t gsg_quantize_act_mx(const uint16_t* X, int T, int K, int fmt, const int32_t* inv_perm, int k,
                                  uint8_t* codes, uint8_t* scales, void* workspace, size_t workspace_bytes,
                                  void* stream);
