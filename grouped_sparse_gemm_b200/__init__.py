@@ -5,6 +5,10 @@ functions keep the ABI's names without the ``gsg_`` prefix and only marshal argu
 provides device memory and the current stream, every step runs in the library's CUDA kernels.
 There is no CPU fallback: if the library is missing or no GPU is present the calls raise.
 
+Beside that path: the router (moe_gate), the residual RMS norm with microscaled output (add_rmsnorm_mx) and
+the same grouped product on OCP microscaled weights (pack_mxfp4, pack_mxfp4_codes -> quantize_act_mx ->
+grouped_mx_gemm).
+
 The path (after "Hardware-Native Joint Sparse-Quantization for Trillion-Scale Mixture-of-Experts",
 paperlayer.ai summary, §3.4 and §D.1): pack_sparse_nvfp4 (offline weights) ->
 moe_route_permute -> quantize_act_nvfp4 -> grouped_sparse_gemm -> unpermute_scale
@@ -265,13 +269,14 @@ PACKED_FILE_VERSION = 1
 
 
 def save_packed(w, path: str) -> None:
-    """Packed weights (PackedSparseWeights or PackedDenseWeights, any device) to an .npz file: the
-    packed bytes exactly as the GEMM reads them, the per-expert FP32 tensor scales, E, N, K and
-    the format.  No re-encoding: load_packed gives back the same bytes."""
+    """Packed weights (PackedSparseWeights, PackedDenseWeights or PackedMxWeights, any device) to an .npz
+    file: the packed bytes exactly as the GEMM reads them, the per-expert FP32 tensor scales (the MXFP4
+    weights have none), E, N, K and the format.  No re-encoding: load_packed gives back the same bytes."""
     import numpy as np
-    fmt = "sparse" if isinstance(w, PackedSparseWeights) else "dense"
+    fmt = "sparse" if isinstance(w, PackedSparseWeights) else "mxfp4" if isinstance(w, PackedMxWeights) else "dense"
+    scale = {} if fmt == "mxfp4" else {"w_scale": w.w_scale.detach().cpu().numpy()}
     np.savez(path, version=PACKED_FILE_VERSION, format=fmt, E=w.E, N=w.N, K=w.K,
-             packed=w.packed.detach().cpu().numpy(), w_scale=w.w_scale.detach().cpu().numpy())
+             packed=w.packed.detach().cpu().numpy(), **scale)
 
 
 def load_packed(path: str, device=None):
@@ -285,8 +290,8 @@ def load_packed(path: str, device=None):
                              f"{PACKED_FILE_VERSION}")
         fmt = str(d["format"])
         E, N, K = int(d["E"]), int(d["N"]), int(d["K"])
-        packed, w_scale = d["packed"], d["w_scale"]
-    if fmt not in ("sparse", "dense"):
+        packed, w_scale = d["packed"], None if fmt == "mxfp4" else d["w_scale"]
+    if fmt not in ("sparse", "dense", "mxfp4"):
         raise ValueError(f"{path}: unknown packed format {fmt!r}")
     # the shape rule of the packers (whole 128-row n-tiles, whole 256-wide K chunks, int range),
     # checked before the byte count so that a wrong N or K of the right size is still rejected
@@ -296,12 +301,15 @@ def load_packed(path: str, device=None):
         raise ValueError(f"{path}: E={E} N={N} K={K} is not a packed shape (E >= 1, N a multiple of 128, "
                          f"K a multiple of 256)")
     L = lib()
-    need = L.gsg_sparse_packed_bytes(E, N, K) if fmt == "sparse" else L.gsg_dense_packed_bytes(E, N, K)
+    need = {"sparse": L.gsg_sparse_packed_bytes, "dense": L.gsg_dense_packed_bytes,
+            "mxfp4": L.gsg_mx_packed_bytes}[fmt](E, N, K)
     if packed.dtype != np.uint8 or packed.ndim != 1 or packed.size != need:
         raise ValueError(f"{path}: {packed.size} packed bytes, expected {need} for {fmt} E={E} N={N} K={K}")
+    pk = torch.from_numpy(packed.copy()).to(device or "cpu")
+    if fmt == "mxfp4":
+        return PackedMxWeights(packed=pk, E=E, N=N, K=K)
     if w_scale.dtype != np.float32 or w_scale.shape != (E,):
         raise ValueError(f"{path}: tensor scales of shape {w_scale.shape} / {w_scale.dtype}, expected ({E},) float32")
-    pk = torch.from_numpy(packed.copy()).to(device or "cpu")
     ws = torch.from_numpy(w_scale.copy()).to(device or "cpu")
     cls = PackedSparseWeights if fmt == "sparse" else PackedDenseWeights
     return cls(packed=pk, w_scale=ws, E=E, N=N, K=K)
@@ -695,6 +703,11 @@ def grouped_mx_gemm(act: MxActivations, w: PackedMxWeights, offsets: torch.Tenso
         raise ValueError(f"activations have K = {act.K}, weights K = {w.K}")
     if offsets.dtype != torch.int32 or offsets.numel() != w.E + 1:
         raise ValueError(f"offsets: int32 of {w.E + 1} entries wanted")
+    if act.codes.numel() != act.R * act.K * act.fmt // 8 or act.scales.numel() != act.K // 8 * act.R:
+        raise ValueError(f"activations: {act.codes.numel()} codes' and {act.scales.numel()} scales' bytes are not R = "
+                         f"{act.R}, K = {act.K}, fmt = {act.fmt}")
+    if w.packed.numel() != w.E * w.N * w.K // 32 * 17:
+        raise ValueError(f"weights: {w.packed.numel()} bytes are not E = {w.E}, N = {w.N}, K = {w.K}")
     if out is not None:
         out_dtype = out.dtype
     if out_dtype not in (torch.bfloat16, torch.float32):

@@ -11,7 +11,11 @@
 // comparison closer than their error bound in 64 bits.  Equal logits with equal biases are equal scores,
 // so they need no second look.
 //
-// One warp per token, expert e in register e / 32 of lane e % 32.
+// One warp per token, expert e in register e / 32 of lane e % 32.  The k-th largest of the 32 lanes' maxima (a
+// warp-wide sort) is no more than the k-th largest choice, so the few experts that come up to it (less the error
+// bound) hold the answer: they are gathered, one to a lane, and ranked by counting, in 64 bits where two are
+// close.  Large batches are bound by instructions issued, about 620 a token (70 % of the issue slots): 65,536
+// tokens x 384 experts 55 us = 1.9 TB/s (k rounds of a warp-wide maximum instead: 257 us).  One token: 3.1 us, launch.
 #include "gsg_internal.cuh"
 #include "gsg_launch.h"
 
@@ -231,7 +235,7 @@ moe_gate_kernel(const GateParams p) {
     b[i] = e < p.E ? bias_of(p, e) : neg_inf();
     if (!(b[i] < INFINITY)) { bad = true; b[i] = neg_inf(); }
   }
-  for (int t = blockIdx.x * kGateWarps + warp; t < p.T; t += gridDim.x * kGateWarps) {
+  for (unsigned t = blockIdx.x * kGateWarps + warp; t < (unsigned)p.T; t += gridDim.x * kGateWarps) {
     const size_t row = (size_t)t * p.E;
     float c[NV];   // the logits, then the choices (experts that do not exist: the lowest number, until the bias)
     float probe = 0.0f, mx = neg_inf();

@@ -20,6 +20,16 @@
 //               logical sparse / 64 dense) and one tcgen05.commit; up to eight TMEM accumulators.
 //   warps 3..6  epilogue: tcgen05.ld accumulator lanes, multiply by s_x * s_w[e], store rows of Y.
 //   warps 11..14 (wide pair tiles only) a second epilogue, for the tile's second n-tile pair.
+// The microscaled formats (see kFmtMx4) differ in four things.  Their scales come as copies of their own, so a
+// last warp produces them into a ring of their own, ahead of the operands.  The copies of both CTAs of a pair
+// complete on the leader's barriers.  Tiles past 64 tokens are wide pair tiles of 128 or 192 tokens
+// (mx_pick_bn) for any N, whose last group of n-tiles may be short.  And an expert's token tiles share its rows
+// evenly.
+// What a stage costs is the MMA warp's instructions as much as the tensor pipe: by SM clock, with operands that
+// the compiler does not know to be warp-uniform, a wide stage took 800 cycles (120 for each of the two barriers,
+// 50 for each MMA) whatever its tokens; with uniform() 620 at 128 tokens and the tensor pipe's 768 at 192.  Copying
+// the scales into TMEM with tcgen05.cp from that warp instead of the loader warps: 10 % slower (4096 x 4096 x 7168,
+// 4-bit: 63 -> 74 us), the copies and the MMAs share a pipe.
 // Every TMA and tcgen05 instruction is issued by an elected lane of a converged warp.
 // 128-token tiles run on CTA pairs (cta_group::2, M = 256 weight rows).  Where N holds whole
 // groups of four n-tiles, a pair tile is wide: 512 weight rows (two MMAs per k-block into two
@@ -925,7 +935,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
                           kMxCodeBytes + kc % kCPB * (G::kSfPerChunk * 512),
                       (nch < kCPB ? nch : kCPB) * (G::kSfPerChunk * 512u), fb);
         tma_load_2d_lane(lane > 31 - G::kSfbA, st + G::kScaleOffB + (31 - lane) * (G::kSfps * 512), &tmap_sfb,
-                         4 * (c.r0 + 128 * (31 - lane)), kc * G::kSfPerChunk, fb);
+                         2 * (c.r0 + 128 * (31 - lane)), kc * G::kSfPerChunk, fb);
         ++g;
         if (++s == kScaleRing) { s = 0; ph ^= 1u; }
       }
@@ -1000,7 +1010,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
             const int t = lane / nch, ch = lane - t * nch;
             bulk_g2s_lane(lane < G::kNT * nch, st + G::kOffW + (t * G::kCPS + ch) * G::kCB,
                           (t == 0 ? wsrc : wsrc_up) + (size_t)(kc + ch) * G::kCB, G::kCB, fb);
-            tma_load_2d_lane(lane == 31, st + G::kOffSFB, &tmap_sfb, 4 * c.r0, kc * G::kSfPerChunk, fb);
+            tma_load_2d_lane(lane == 31, st + G::kOffSFB, &tmap_sfb, 2 * c.r0, kc * G::kSfPerChunk, fb);
           }
         } else {
           // activation codes: lane ch * nb + b copies box b (64-row boxes first) of chunk ch
@@ -1765,13 +1775,13 @@ int launch_gemm(int fmt, const uint8_t* a_codes, const uint8_t* a_scales, const 
       return 2;
   }
   {
-    // activation scale quad entries as a [KBa][rcap * 4] tensor of 32-bit words; one box = the stage's atoms
-    // (32 entries of 16 bytes are one row of a box)
-    cuuint64_t dims[2] = {(cuuint64_t)rcap * 4u, (cuuint64_t)KBa};
+    // activation scale quad entries as a [KBa][rcap * 2] tensor of 64-bit words (an entry is two; coordinates
+    // stay within 31 bits for R <= 2^30); one box = the stage's atoms, 32 entries to a row
+    cuuint64_t dims[2] = {(cuuint64_t)rcap * 2u, (cuuint64_t)KBa};
     cuuint64_t strides[1] = {(cuuint64_t)rcap * 16u};
-    cuuint32_t box[2] = {128u, (cuuint32_t)sfps};
+    cuuint32_t box[2] = {64u, (cuuint32_t)sfps};
     cuuint32_t estr[2] = {1u, 1u};
-    if (enc(&ts, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<uint8_t*>(a_scales), dims, strides, box, estr,
+    if (enc(&ts, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, const_cast<uint8_t*>(a_scales), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return 2;

@@ -110,7 +110,9 @@ cudaError_t launch_pack_mxfp4_codes(const uint8_t* codes, const uint8_t* scales,
 
 // ------------------------------------------------------------------ activation quantizer + dispatch
 // A lane makes 16 bytes of codes: a whole 32-block in 4 bits, half of one in 8 bits (two lanes share the
-// block's maximum).  Every token is read and quantized once and written to its k routed rows.
+// block's maximum).  Every token is read and quantized once and written to its k routed rows.  Bound by the scattered
+// scale words' sectors and the codes' writes: 512 tokens x 8 rows x 2048, 4-bit, 4.5 us; 1023 rows x 7168, 8-bit,
+// 5.6 us; 1368 tokens x 8 x 7168, 4-bit, 18 us (3.4 TB/s of what it has to move).
 struct MxQuantParams {
   const uint16_t* X;
   const int32_t* inv_perm;

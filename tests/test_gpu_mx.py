@@ -254,6 +254,31 @@ def test_product_long_output(gsg):
     tl.assert_gemm_close(y[r], yr, b, "long output")
 
 
+@pytest.mark.parametrize("fmt", [4, 8])
+def test_product_hint_below_the_truth(gsg, fmt):
+    """The hint sets the tile, never the result: experts with more rows than it says."""
+    check_product(gsg, [40, 0, 130, 3], 384, 512, fmt, 4, sample=24)
+    check_product(gsg, [300] * 3 + [2] * 60, 1024, 256, fmt, 30, sample=8)
+    check_product(gsg, [2] * 40, 4096, 256, fmt, 1)          # (runs of tiles by bytes)
+
+
+@pytest.mark.parametrize("fmt", [4, 8])
+@pytest.mark.parametrize("n,hint", [(3, 16), (150, -1)])
+def test_product_many_experts(gsg, fmt, n, hint):
+    """E = 1024: the expert tables take shared memory from the ring."""
+    E, N, K = 1024, 128, 256
+    codes, sc = weights(4, N, K)
+    i = np.arange(E) % 4
+    w = pack(gsg, codes[i], sc[i])
+    X = torch.randn(E * n, K, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    off = torch.arange(E + 1, dtype=torch.int32, device=DEV) * n
+    y = gsg.grouped_mx_gemm(gsg.quantize_act_mx(X.to(DEV), fmt), w, off, hint)
+    for e in (0, 1, 511, 1023):
+        q, s = omx.quantize(X[e * n:(e + 1) * n].double().numpy(), fmt)
+        yr, b = ogemm.gemm_rows(omx.dequantize(q, s, fmt), omx.dequantize(codes[e % 4], sc[e % 4], 4), 1.0)
+        tl.assert_gemm_close(y[e * n:(e + 1) * n], yr, b, f"expert {e}")
+
+
 # ------------------------------------------------------------------ as a program uses them
 def test_streams_graphs_and_own_outputs(gsg):
     rows, N, K = [40, 0, 70, 90], 512, 512

@@ -161,3 +161,25 @@ def test_binding_refuses_wrong_shapes_and_types():
 def test_binding_refuses_cpu_tensors():
     with pytest.raises((ValueError, RuntimeError, AssertionError)):
         gsg.quantize_act_mx(torch.zeros(4, 256, dtype=torch.bfloat16))
+
+
+def test_packed_mx_storage(tmp_path):
+    w = gsg.PackedMxWeights((torch.arange(2 * 3 * 17408) % 253).to(torch.uint8), 2, 128, 768)
+    p = str(tmp_path / "w.npz")
+    gsg.save_packed(w, p)
+    r = gsg.load_packed(p)
+    assert isinstance(r, gsg.PackedMxWeights) and (r.E, r.N, r.K) == (2, 128, 768) and torch.equal(r.packed, w.packed)
+    gsg.save_packed(gsg.PackedMxWeights(w.packed[:-1], 2, 128, 768), p)
+    with pytest.raises(ValueError):
+        gsg.load_packed(p)
+
+
+def test_product_refuses_buffers_of_another_size():
+    off = torch.zeros(2, dtype=torch.int32)
+    codes, scales = torch.zeros(4, 256, dtype=torch.uint8), torch.zeros(128, dtype=torch.uint8)
+    w = gsg.PackedMxWeights(torch.zeros(17408, dtype=torch.uint8), 1, 128, 256)
+    for act, ww in ((gsg.MxActivations(codes, scales, 5, 256, 8), w), (gsg.MxActivations(codes, scales, 4, 256, 4), w),
+                    (gsg.MxActivations(codes, scales[:64], 4, 256, 8), w),
+                    (gsg.MxActivations(codes, scales, 4, 256, 8), gsg.PackedMxWeights(w.packed[:100], 1, 128, 256))):
+        with pytest.raises(ValueError):
+            gsg.grouped_mx_gemm(act, ww, off)
