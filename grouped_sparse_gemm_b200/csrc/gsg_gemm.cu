@@ -497,20 +497,17 @@ __device__ __forceinline__ TileDesc decode_tile(int t, const int* pref, const in
 //    one token tile and the CTAs hold dozens of tiles (decode batches of 32-256 tokens on 384
 //    experts: 5-10 % faster); with several token tiles per expert it loses the sharing above
 //    (the 30B and 1T prefill GEMMs ran 20-60 % slower), and with a handful of tiles per CTA
-//    (one token on 8 experts) it measured 20 % slower.  A reversed-order (snake) round-robin,
+//    (one token on 8 experts) it measured 20 % slower; microscaled wide tiles, 64 experts x 4096 x 7168 with
+//    10944 rows: 214 us round-robin, 294 us in runs.  A reversed-order (snake) round-robin,
 //    tried for the load balance of heavy token tiles, measured slower than the plain one.
 constexpr int kSchedRoundRobin = 0;
 constexpr int kSchedRuns = 1;
-//  kSchedRotate: round-robin whose rounds each start one unit further on.  Where experts have, say, one full
-//    and one short token tile, plain round-robin over an even number of units hands some units only full
-//    ones.
-constexpr int kSchedRotate = 2;
 
 // `unit` / `nunits`: this CTA's index and the number of CTAs, or for CTA pairs the pair's index
 // and the number of pairs (both CTAs of a pair take the same tiles).
 __device__ __forceinline__ int tile_of(int j, int sched, int tb, int unit, int nunits) {
   if (sched == kSchedRuns) return tb + j;
-  return j * nunits + (sched == kSchedRotate ? (unit + j) % nunits : unit);
+  return j * nunits + unit;
 }
 
 // The j-th tile of this CTA: from the shared-memory table filled at set-up, or decoded on the
@@ -890,9 +887,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
     int rest = total_tiles - rounds * nunits;
     if (rest < 0) { --rounds; rest += nunits; }
     if (rest >= nunits) { ++rounds; rest -= nunits; }
-    // this unit's place in the last round
-    const int at = p.sched == kSchedRotate ? (unit + rounds) % nunits : unit;
-    n_my = uniform(rounds + (at < rest ? 1 : 0));
+    n_my = uniform(rounds + (unit < rest ? 1 : 0));
   }
   // this CTA's tiles, decoded once
   for (int j = threadIdx.x; j < n_my && j < p.tcap; j += blockDim.x) {
@@ -1740,8 +1735,7 @@ int launch_gemm(int fmt, const uint8_t* a_codes, const uint8_t* a_scales, const 
   // round-robin
   const long long touched_max = R < E ? R : E;
   const int sched = (!pair && max_rows > 0 && max_rows <= BN && touched_max * NTt >= 32LL * units) ? kSchedRuns
-                    : fmt_mx(fmt) && BN >= 128                                                     ? kSchedRotate
-                                                                                                   : kSchedRoundRobin;
+                                                                                                  : kSchedRoundRobin;
   long long tcap;
   if (sched == kSchedRuns) {
     // a CTA's share of the bytes holds at most (wc + BN ac) / (wc + ac) times the average tile count
