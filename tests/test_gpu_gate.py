@@ -203,3 +203,12 @@ def test_many_tokens(gsg):
         assert torch.equal(ids.cpu().long(), order)
         w = p.gather(1, order)
         torch.testing.assert_close(gates.cpu().double(), w / w.sum(1, keepdim=True), rtol=2.0 ** -23 * 20, atol=0)
+
+
+def test_long_batch(gsg):
+    """Offsets past 2^32 bytes in the logits."""
+    x = randn(1000, 256, 3).to(DEV)
+    ids, gates = gsg.moe_gate(x.repeat(5000, 1), 4, "sigmoid")
+    i1, g1 = gsg.moe_gate(x, 4, "sigmoid")
+    assert torch.equal(ids.view(5000, 1000, 4), i1.expand(5000, -1, -1))
+    assert torch.equal(gates.view(5000, 1000, 4), g1.expand(5000, -1, -1))

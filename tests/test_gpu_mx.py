@@ -279,6 +279,43 @@ def test_product_many_experts(gsg, fmt, n, hint):
         tl.assert_gemm_close(y[e * n:(e + 1) * n], yr, b, f"expert {e}")
 
 
+@pytest.mark.parametrize("fmt", [4, 8])
+@pytest.mark.parametrize("hint", [3, 1])
+def test_product_runs_of_tiles(gsg, fmt, hint):
+    """Enough tiles per CTA for the schedule by bytes; with a hint below the truth too (20-row experts)."""
+    E, N, K = 128, 4864, 256
+    codes, sc = weights(2, N, K)
+    i = np.arange(E) % 2
+    w = pack(gsg, codes[i], sc[i])
+    rows = np.full(E, 3) if hint == 3 else np.where(np.arange(E) % 9 == 4, 20, 1)
+    off = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    X = torch.randn(int(off[-1]), K, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    y = gsg.grouped_mx_gemm(gsg.quantize_act_mx(X.to(DEV), fmt), w, torch.from_numpy(off).to(DEV), hint)
+    q, s = omx.quantize(X.double().numpy(), fmt)
+    A = omx.dequantize(q, s, fmt)
+    W = [omx.dequantize(codes[e], sc[e], 4) for e in range(2)]
+    for e in range(E):
+        yr, b = ogemm.gemm_rows(A[off[e]:off[e + 1]], W[e % 2], 1.0)
+        tl.assert_gemm_close(y[off[e]:off[e + 1]], yr, b, f"expert {e}")
+
+
+@pytest.mark.parametrize("fmt", [4, 8])
+def test_quantize_long(gsg, fmt):
+    """Offsets past 2^32 bytes (and the two-launch scales of rows in token order)."""
+    T, K = 270000, 16384
+    x = torch.randn(1000, K, device=DEV).to(torch.bfloat16)
+    X = x.repeat(270, 1)
+    a = gsg.quantize_act_mx(X, fmt)
+    codes, sc = omx.quantize(x.double().cpu().numpy(), fmt)
+    codes = torch.from_numpy(omx.pack_nibbles(codes) if fmt == 4 else codes).to(DEV)
+    for t0 in (0, 130000, 262000, 269000):
+        assert torch.equal(a.codes[t0:t0 + 1000], codes)
+    quad = a.scales.view(K // 128, T, 4, 4)
+    words = torch.from_numpy(sc).to(DEV).view(1000, K // 128, 4).transpose(0, 1)
+    assert torch.equal(quad[:, 269000:, 0], words) and torch.equal(quad[:, 262000:262968, 1], words[:, 32:])
+    assert (quad[:, -32:, 1] == 0).all() and (quad[:, -96:, 3] == 0).all()
+
+
 # ------------------------------------------------------------------ as a program uses them
 def test_streams_graphs_and_own_outputs(gsg):
     rows, N, K = [40, 0, 70, 90], 512, 512

@@ -163,3 +163,17 @@ def test_norm_many_rows(gsg):
     codes, sc = omx.quantize(definition(x, torch.ones(256), None, 1e-6)[1].numpy(), 8)
     np.testing.assert_array_equal(n.act.codes.cpu().numpy(), codes)
     np.testing.assert_array_equal(n.act.scales.cpu().numpy(), omx.quad_scales(sc).reshape(-1))
+
+
+def test_norm_long(gsg):
+    """Offsets past 2^32 bytes in every input and output."""
+    T, K = 270000, 16384
+    x = rows(1000, K, 1).to(DEV)
+    w = torch.ones(K, device=DEV)
+    n = gsg.add_rmsnorm_mx(x.repeat(270, 1), w, residual=x.repeat(270, 1))
+    m = gsg.add_rmsnorm_mx(x, w, residual=x)
+    for t0 in (0, 131000, 262000, 269000):
+        for a, b in ((n.h, m.h), (n.y, m.y), (n.act.codes, m.act.codes)):
+            assert torch.equal(a[t0:t0 + 1000], b)
+    long, short = n.act.scales.view(K // 128, T, 4, 4), m.act.scales.view(K // 128, 1000, 4, 4)
+    assert torch.equal(long[:, -1000:], short) and torch.equal(long[:, 262000:263000, 0], short[:, :, 0])
