@@ -10,7 +10,7 @@
 // around one shared-memory ring whose stages hold 256 to 768 logical K of one tile (weights,
 // activation codes and both scales):
 //   warp 0      weight producer: per stage one bulk copy per interleaved packed weight block and
-//               one 3-D TMA box of the activation scale atoms, each from its own lane.
+//               one TMA box of the activation scale atoms, each from its own lane.
 //   warp 2      activation producer: tensor-map TMA boxes (128B swizzle, 64 or 32 rows) of only the
 //               token rows the tile holds, each from its own lane.
 //   warps 7..10 scale/metadata loaders, one per TMEM lane quadrant: read the stage's metadata and
