@@ -1551,13 +1551,13 @@ int gemm_pick_bn(int max_rows, int R, int E) {
 
 // Token tile of the microscaled formats.  Up to 32 rows in every expert: the smallest tile that holds them,
 // one CTA per tile.  Beyond: 64 tokens on one CTA, or 128 or 192 on a wide pair tile, whichever an estimate in
-// SM cycles makes cheaper for experts of R / E rows each (measured by SM clock, 1.9 GHz).  `chunks` ring
-// stages make a tile; a wide one takes max(620, 4 N) cycles for N tokens (4 N: the tensor pipe's time for
-// 512 x N x one chunk; 620: issuing it), its single accumulator buffer costs 1500 or 3400 more between tiles,
-// and the pair launch about 4000 at its ends; a 64-token stage takes 700 (470 with 8-bit activations, half as
-// long).  Measured, N = 4096, K = 7168, 4-bit, 64 / 128 / 192 tokens: 64 experts x 100 rows 298 / 162 / -,
-// x 171 rows - / 244 / 200, x 300 rows - / 382 / 296 us; one expert x 1023 rows 55 / 19.1 / 21.8 us, x 4096
-// rows - / 57 / 51 us; 8 experts x 100 rows, N = K = 1024: 7.1 / 13.4 / - us.
+// SM cycles (1.9 GHz) makes cheaper for experts of R / E rows each.  `chunks` ring stages make a tile; a wide
+// one takes max(620, 4 N) cycles for N tokens (4 N: the tensor pipe's time for 512 x N x one chunk; 620:
+// issuing it), its single accumulator buffer costs 1500 or 2600 more between tiles, and the pair launch about
+// 4000 at its ends; a 64-token stage takes 700 (470 with 8-bit activations, half as long).  Measured, 4-bit,
+// 64 / 128 / 192 tokens: 32 experts x 100 rows, N = 1280, K = 2048 19.5 / 14.6 / 14.9 us; 8 x 100, N = K = 1024 5.6 /
+// 7.4 / 7.4; 64 x 300, N = 768, K = 2048 44 / 30.5 / 27.7; N = 4096, K = 7168: one expert x 128 rows 13.7 / 16.7 / 17.2,
+// x 1023 rows 43.9 / 18.9 / 20.6, 4 x 1100 rows 164 / 61 / 55.6, 16 x 171 rows 114 / 63 / 52, 16 x 256 rows 144 / 70 / 71.
 static int mx_pick_bn(int max_rows, int R, int E, int N, int chunks, bool act8, int num_sms, int pairs) {
   if (max_rows > 0 && max_rows <= 16) return 16;
   if (max_rows > 0 && max_rows <= 32) return 32;
@@ -1572,7 +1572,7 @@ static int mx_pick_bn(int max_rows, int R, int E, int N, int chunks, bool act8, 
     const long long tokens = ((rows + n - 1) / n + 15) / 16 * 16;
     const long long waves = (n * E * (wide ? (nt + 3) / 4 : nt) + units - 1) / units;
     const long long stage = !wide ? (act8 ? 470 : 700) : 4 * tokens > 620 ? 4 * tokens : 620;
-    const long long cost = (wide ? 4000 : 0) + waves * (chunks * stage + (i == 0 ? 1000 : i == 1 ? 1500 : 3400));
+    const long long cost = (wide ? 4000 : 0) + waves * (chunks * stage + (i == 0 ? 1000 : i == 1 ? 1500 : 2600));
     if (i == 0 || cost < best) { best = cost; bn = bns[i]; }
   }
   return bn;
