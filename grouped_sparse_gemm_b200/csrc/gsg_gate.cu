@@ -98,6 +98,9 @@ __device__ __forceinline__ float load_logit_if<uint16_t>(const uint16_t* p, int 
   return bf16_bits_to_f32(v);
 }
 
+template <typename T>
+__device__ __forceinline__ float lowest_logit() { return __uint_as_float(sizeof(T) == 4 ? 0xFF7FFFFFu : 0xFF7F0000u); }
+
 __device__ __forceinline__ float bias_of(const GateParams& p, int e) {
   return p.bias != nullptr ? __ldg(p.bias + e) : 0.0f;
 }
@@ -264,6 +267,8 @@ moe_gate_kernel(const GateParams p) {
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) s = __fadd_rn(s, fast_exp(__fsub_rn(c[i], mx)));
+        // (a row of the lowest number throughout: what stands for missing experts counted as much as they do, 1 each)
+        if (mx == lowest_logit<T>()) s -= (float)__popc(~(there | closed) & (0xFFFFFFFFu >> (32 - NV)));
         inv_sum = __frcp_rn(warp_sum(s));
       }
     }
