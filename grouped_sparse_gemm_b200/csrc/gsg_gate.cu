@@ -152,8 +152,9 @@ struct ExactChoice {
 };
 
 // Group scores: lanes_per_group lanes walk a group's choices (value(e)), then merge their two largest.
+// size: the sum of the terms' magnitudes, which the error of the score goes by.
 template <typename V, typename F>
-__device__ __forceinline__ V group_score(const GateParams& p, int lane, int lpg, F value) {
+__device__ __forceinline__ V group_score(const GateParams& p, int lane, int lpg, F value, V* size) {
   const int g = lane / lpg, sub = lane % lpg;
   V a = -INFINITY, b = -INFINITY;   // the two largest
   if (g < p.n_group)
@@ -172,7 +173,10 @@ __device__ __forceinline__ V group_score(const GateParams& p, int lane, int lpg,
     b = b > b2 ? b : b2;
     b = b > lo ? b : lo;
   }
-  return p.group_top == 2 ? a + b : a;
+  *size = p.group_top == 2 ? fabs(a) + fabs(b) : fabs(a);
+  const V sum = p.group_top == 2 ? a + b : a;
+  // (a sum below the range is the lowest number, for -inf is a group without group_top available experts)
+  return sum == -INFINITY && b > -INFINITY ? (V)-3.402823466e38f : sum;
 }
 
 // Bit g set: group g is among the topk_group best (ties to the lowest index).  tol >= 0: *close is set
@@ -307,13 +311,14 @@ moe_gate_kernel(const GateParams p) {
       for (int i = 0; i < NV; ++i)
         if (32 * i + lane < p.E) sh[32 * i + lane] = c[i];
       __syncwarp();
-      const float score = group_score<float>(p, lane, lpg, SharedChoice{sh});
+      float size = 0.0f;   // (twice its error: the terms' and the sum's rounding, and that of two scores)
+      const float score = group_score<float>(p, lane, lpg, SharedChoice{sh}, &size);
       bool close = false;
-      kept = keep_groups<float>(p, lane, lpg, score,
-                                p.by_score ? __fmaf_rn(fabsf(score), 0x1p-20f, 2.0f * tol) : -1.0f, &close);
+      kept = keep_groups<float>(p, lane, lpg, score, p.by_score ? __fmaf_rn(size, 0x1p-20f, 2.0f * tol) : -1.0f, &close);
       if (close && p.by_score) {
         exact_sum();
-        const double score64 = group_score<double>(p, lane, lpg, exact);
+        double size64;
+        const double score64 = group_score<double>(p, lane, lpg, exact, &size64);
         kept = keep_groups<double>(p, lane, lpg, score64, -1.0, &close);
       }
 #pragma unroll
