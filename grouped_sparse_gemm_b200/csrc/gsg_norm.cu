@@ -56,7 +56,8 @@ __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
 // format, so rounding it again to fewer bits gives what rounding v + rest would have given.
 __device__ __forceinline__ float round_odd(float v, float rest) {
   uint32_t u = __float_as_uint(v);
-  u -= (uint32_t)(__fmul_rn(v, rest) < 0.0f);   // towards zero: v was rounded away from it
+  // towards zero where v was rounded away from it: rest, signed by v, is negative (a product of the two may underflow)
+  u -= (uint32_t)(__uint_as_float(__float_as_uint(rest) ^ (u & 0x80000000u)) < 0.0f);
   u |= (uint32_t)(rest != 0.0f);
   return __uint_as_float(u);
 }

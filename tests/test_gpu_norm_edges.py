@@ -38,3 +38,17 @@ def test_weights_past_the_middle_of_the_range(gsg, dtype):
     x[2, 8:] = 0.0
     for up, wp in ((40, 88), (59, 70), (50, 100), (-40, -100), (-55, -60), (0, 119), (0, -95), (0, 60)):
         check_nearest(gsg, (x.double() * 2.0 ** up).to(BF), (unit.double() * 2.0 ** wp).to(dtype), 0.0)
+
+
+@pytest.mark.parametrize("power", [0, -30, -51, -62, -70, -90, -100])
+def test_values_next_to_a_border(gsg, power):
+    """A row of ones with eps 2^-30 has y = w (1 - 2^-31): weights on the borders between bf16 numbers and between
+    codes give values just inside them, which fp32 rounds onto the border."""
+    K = 512
+    borders = torch.cat([1 + (2 * torch.arange(128) + 1) * 2.0 ** -8,      # midpoints of bf16 numbers
+                         1 + (2 * torch.arange(8) + 1) * 2.0 ** -4,        # of E4M3 numbers
+                         torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0])]).float()
+    w = borders.repeat(4)[:K] * torch.where(torch.arange(K) % 3 == 0, -1.0, 1.0)
+    x = torch.ones(3, K, dtype=BF)
+    x[1] = -1.0
+    check_nearest(gsg, x, w * 2.0 ** power, 2.0 ** -30)
