@@ -62,6 +62,14 @@ __device__ __forceinline__ float round_odd(float v, float rest) {
   return __uint_as_float(u);
 }
 
+// The larger of two, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+constexpr uint32_t kBf16Inf = 0x7F7F8000u;   // the least magnitude that bf16 has no finite number for
+
 constexpr int kNormThreads = 512;
 
 // kRes: 0 no residual, 1 bf16, 2 fp32.  kBits: 0 no microscaled output, 4, 8.  A thread holds kU units
@@ -143,7 +151,12 @@ add_rmsnorm_kernel(const NormParams p) {
   __syncthreads();
   sum = warp_sum_d(lane < nw ? red[lane] : 0.0);
   const double var = sum / (double)p.K + (double)p.eps;
-  if (!(var < (double)INFINITY) && threadIdx.x == 0) set_status(p.status, GSG_ERR_NONFINITE);
+  if (kBits == 0 && p.y == nullptr) {   // h alone
+    if (!(var < (double)INFINITY) && threadIdx.x == 0) set_status(p.status, GSG_ERR_NONFINITE);
+    return;
+  }
+  // (the units below find such a row too; with two of them the branch keeps the compiler within the registers)
+  if (kU == 2 && !(var > 0.0 && var < (double)INFINITY) && threadIdx.x == 0) set_status(p.status, GSG_ERR_NONFINITE);
   const double rd = rsqrt(var);
   const float rh = (float)rd, rl = (float)(rd - (double)rh);
   if (kU == 2) {   // (with two units a thread it costs the registers of a third block)
@@ -186,17 +199,19 @@ add_rmsnorm_kernel(const NormParams p) {
         y[j] = round_odd(s, (float)(d - (double)s));
       }
     }
+    // a y that is not finite, as every one is of a row without a norm (v 0, infinite or NaN), or that bf16 does not hold
+    float top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(y[j]));
+    uint32_t am = __float_as_uint(top);
+    if (am >= kBf16Inf) set_status(p.status, GSG_ERR_NONFINITE);
     if (p.y != nullptr && in)
       reinterpret_cast<uint4*>(p.y + row)[u] =
           make_uint4(pack2_bf16(y[0], y[1]), pack2_bf16(y[2], y[3]), pack2_bf16(y[4], y[5]), pack2_bf16(y[6], y[7]));
     if (kBits != 0) {
       constexpr int kB = kBits == 0 ? 8 : kBits;
-      uint32_t am = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) am = max(am, abs_bits(y[j]));
       am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
       am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-      if (am >= kF32Inf) set_status(p.status, GSG_ERR_NONFINITE);
       const uint32_t sc = mx_scale_byte<kB>(am);
       const float inv = mx_inv_scale(sc);
 #pragma unroll

@@ -335,9 +335,10 @@ gsg_status_t gsg_quantize_act_mx(const uint16_t* X, int T, int K, int fmt, const
  * residual's own buffer); weight [K] in weight_dtype.  y bf16 [T][K], or NULL when it is not wanted.
  * fmt GSG_MXFP4 or GSG_MXFP8: codes and scales of the unrounded y, rows in token order, as
  * gsg_grouped_mx_gemm takes them; 0: none (codes, scales unused).  The mean square is summed in more than
- * 32 bits.  K % 8 == 0 (% 256 with codes), K <= 32768, else GSG_ERR_UNSUPPORTED_SHAPE; eps >= 0 (a row of
- * zeros with eps 0 has no norm: GSG_ERR_NONFINITE, like every non-finite row).  All pointers 16-byte
- * aligned.  No workspace. */
+ * 32 bits; weights may have any finite size.  K % 8 == 0 (% 256 with codes), K <= 32768, else
+ * GSG_ERR_UNSUPPORTED_SHAPE; eps >= 0.  GSG_ERR_NONFINITE, whatever the outputs: an infinite or NaN h; where y
+ * or codes are wanted, a row of zeros with eps 0 (it has no norm), a weight that is not finite, and a y past
+ * bf16's largest number.  All pointers 16-byte aligned.  No workspace. */
 gsg_status_t gsg_add_rmsnorm_mx(const uint16_t* x, const void* residual, int residual_dtype, const void* weight,
                                 int weight_dtype, int T, int K, float eps, void* h, uint16_t* y, int fmt,
                                 uint8_t* codes, uint8_t* scales, void* stream);

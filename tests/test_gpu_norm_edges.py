@@ -52,3 +52,35 @@ def test_values_next_to_a_border(gsg, power):
     x = torch.ones(3, K, dtype=BF)
     x[1] = -1.0
     check_nearest(gsg, x, w * 2.0 ** power, 2.0 ** -30)
+
+
+def test_every_output_reports_what_is_not_finite(gsg):
+    """Rows without a norm, weights and products that are not finite, with and without codes, with y or h alone."""
+    K = 256
+    x = rows(4, K, 1).to(DEV)
+    w = torch.ones(K, device=DEV)
+
+    def status(x, w, eps=1e-6, **kw):
+        gsg.add_rmsnorm_mx(x, w, eps=eps, **kw)
+        return gsg.get_device_status()
+    outputs = (dict(fmt=None), dict(fmt=8), dict(fmt=4, want_y=False))
+    for kw in outputs:
+        assert status(x, w, **kw) == 0
+        assert status(torch.zeros_like(x), w, eps=0.0, **kw) == -5          # a row of zeros has no norm
+        assert status(torch.zeros_like(x), w, **kw) == 0
+        for v in (float("nan"), INF):
+            y, u = x.clone(), w.clone()
+            y[2, 3] = v
+            u[7] = v
+            assert status(y, w, **kw) == -5
+            assert status(x, u, **kw) == -5
+        big = torch.zeros(1, K, dtype=BF, device=DEV)
+        big[0, 0] = 1.0                                                     # h / rms = 16
+        assert status(big, w * 2.0 ** 123, **kw) == 0
+        assert status(big, w * 2.0 ** 126, **kw) == -5                      # y past the fp32 range
+    r = x.float().clone()
+    r[1, 1] = INF
+    assert status(x, w, residual=r, fmt=None, want_y=False) == -5           # the residual stream alone
+    bad = w.clone()
+    bad[0] = INF                                                            # (the weight has no part in it)
+    assert status(x, bad, residual=x.float(), fmt=None, want_y=False) == 0
