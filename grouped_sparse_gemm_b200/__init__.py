@@ -3,6 +3,8 @@
 Thin Python binding over the C ABI of ``libgsg.so`` (declared in ``include/gsg.h``).  The
 functions keep the ABI's names without the ``gsg_`` prefix and only marshal arguments: torch
 provides device memory and the current stream, every step runs in the library's CUDA kernels.
+A call given a `stream` runs there: its outputs and workspaces come from that stream's memory, and the caller
+keeps its inputs until it has run and lets other streams wait for it.
 There is no CPU fallback: if the library is missing or no GPU is present the calls raise.
 
 Beside that path: the router (moe_gate), the residual RMS norm with microscaled output (add_rmsnorm_mx) and
@@ -147,6 +149,28 @@ def _stream(stream: Optional[torch.cuda.Stream] = None):
 def _check(fn: str, st: int):
     if st != 0:
         raise GsgError(fn, st)
+
+
+def _tensors(o) -> list:
+    """The tensors of a call's result (a tensor, a tuple, one of the classes below)."""
+    if isinstance(o, torch.Tensor):
+        return [o]
+    return [t for v in (o if isinstance(o, tuple) else vars(o).values() if hasattr(o, "__dict__") else ())
+            for t in _tensors(v)]
+
+
+def _on_stream(fn, stream, *args):
+    """fn(*args), a call of this module, with `stream` current.  What it allocates is that stream's memory: neither
+    what the stream current until now has yet to write, nor given to it while the call still runs.  That stream
+    may read the outputs (once it waits for `stream`), also if they are dropped before it has."""
+    now = torch.cuda.current_stream()
+    if stream.cuda_stream == now.cuda_stream:
+        return fn(*args)
+    with torch.cuda.stream(stream):
+        out = fn(*args)
+    for t in _tensors(out):
+        t.record_stream(now)
+    return out
 
 
 def _need_cuda(*ts: Optional[torch.Tensor]):
@@ -319,6 +343,8 @@ def load_packed(path: str, device=None):
 def pack_sparse_nvfp4(W: torch.Tensor, out: Optional[PackedSparseWeights] = None,
                       workspace: Optional[torch.Tensor] = None, stream=None) -> PackedSparseWeights:
     """W fp32 [E, N, K] -> paired 4:8 NVFP4 packed weights (gsg_pack_sparse_nvfp4)."""
+    if stream is not None:
+        return _on_stream(pack_sparse_nvfp4, stream, W, out, workspace)
     _need_cuda(W)
     assert W.dtype == torch.float32 and W.dim() == 3
     E, N, K = W.shape
@@ -331,13 +357,15 @@ def pack_sparse_nvfp4(W: torch.Tensor, out: Optional[PackedSparseWeights] = None
     need = workspace_size(OP_PACK_SPARSE, E, N, K)
     ws = workspace if workspace is not None else _workspace(need, dev)
     _check("gsg_pack_sparse_nvfp4", L.gsg_pack_sparse_nvfp4(
-        _ptr(W), E, N, K, _ptr(out.packed), _ptr(out.w_scale), _ptr(ws), ws.numel(), _stream(stream)))
+        _ptr(W), E, N, K, _ptr(out.packed), _ptr(out.w_scale), _ptr(ws), ws.numel(), _stream()))
     return out
 
 
 def pack_dense_nvfp4(W: torch.Tensor, out: Optional[PackedDenseWeights] = None,
                      workspace: Optional[torch.Tensor] = None, stream=None) -> PackedDenseWeights:
     """W fp32 [E, N, K] -> dense NVFP4 (16-element blocks) for the control GEMM."""
+    if stream is not None:
+        return _on_stream(pack_dense_nvfp4, stream, W, out, workspace)
     _need_cuda(W)
     assert W.dtype == torch.float32 and W.dim() == 3
     E, N, K = W.shape
@@ -350,13 +378,15 @@ def pack_dense_nvfp4(W: torch.Tensor, out: Optional[PackedDenseWeights] = None,
     need = workspace_size(OP_PACK_DENSE, E, N, K)
     ws = workspace if workspace is not None else _workspace(need, dev)
     _check("gsg_pack_dense_nvfp4", L.gsg_pack_dense_nvfp4(
-        _ptr(W), E, N, K, _ptr(out.packed), _ptr(out.w_scale), _ptr(ws), ws.numel(), _stream(stream)))
+        _ptr(W), E, N, K, _ptr(out.packed), _ptr(out.w_scale), _ptr(ws), ws.numel(), _stream()))
     return out
 
 
 def moe_route_permute(topk_ids: torch.Tensor, E: int, out: Optional[Routing] = None,
                       workspace: Optional[torch.Tensor] = None, stream=None) -> Routing:
     """topk ids int32 [T, k] -> expert offsets, perm_src, inv_perm (gsg_moe_route_permute)."""
+    if stream is not None:
+        return _on_stream(moe_route_permute, stream, topk_ids, E, out, workspace)
     _need_cuda(topk_ids)
     assert topk_ids.dtype == torch.int32 and topk_ids.dim() == 2
     T, k = topk_ids.shape
@@ -371,7 +401,7 @@ def moe_route_permute(topk_ids: torch.Tensor, E: int, out: Optional[Routing] = N
         ws = _workspace(need, dev) if need else None
     _check("gsg_moe_route_permute", lib().gsg_moe_route_permute(
         _ptr(topk_ids), T, k, E, _ptr(out.offsets), _ptr(out.perm_src), _ptr(out.inv_perm),
-        _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+        _ptr(ws), 0 if ws is None else ws.numel(), _stream()))
     return out
 
 
@@ -392,6 +422,8 @@ def quantize_act_nvfp4(X: torch.Tensor, sf_block: int = 32, inv_perm: Optional[t
                        out: Optional[QuantizedActivations] = None,
                        workspace: Optional[torch.Tensor] = None, stream=None) -> QuantizedActivations:
     """X bf16 [T, K] -> NVFP4 codes/scales in routed row order (gsg_quantize_act_nvfp4)."""
+    if stream is not None:
+        return _on_stream(quantize_act_nvfp4, stream, X, sf_block, inv_perm, top_k, x_scale_in, out, workspace)
     _need_cuda(X, inv_perm, x_scale_in)
     assert X.dtype == torch.bfloat16 and X.dim() == 2
     T, K = X.shape
@@ -405,7 +437,7 @@ def quantize_act_nvfp4(X: torch.Tensor, sf_block: int = 32, inv_perm: Optional[t
     ws = workspace if workspace is not None else _workspace(workspace_size(OP_QUANTIZE, 0, 0, K, T, top_k), dev)
     _check("gsg_quantize_act_nvfp4", lib().gsg_quantize_act_nvfp4(
         _ptr(X), T, K, sf_block, _ptr(inv_perm), top_k, _ptr(x_scale_in), _ptr(out.codes),
-        _ptr(out.scales), _ptr(out.x_scale), _ptr(ws), ws.numel(), _stream(stream)))
+        _ptr(out.scales), _ptr(out.x_scale), _ptr(ws), ws.numel(), _stream()))
     return out
 
 
@@ -415,6 +447,9 @@ def moe_dispatch_nvfp4(topk_ids: torch.Tensor, X: torch.Tensor, E: int, sf_block
                        stream=None):
     """moe_route_permute + quantize_act_nvfp4 in one call (gsg_moe_dispatch_nvfp4): the same
     outputs bit for bit, one launch fewer.  Returns (Routing, QuantizedActivations)."""
+    if stream is not None:
+        return _on_stream(moe_dispatch_nvfp4, stream, topk_ids, X, E, sf_block, x_scale_in, out_route, out_act,
+                          workspace)
     _need_cuda(topk_ids, X, x_scale_in)
     assert topk_ids.dtype == torch.int32 and topk_ids.dim() == 2
     assert X.dtype == torch.bfloat16 and X.dim() == 2 and X.shape[0] == topk_ids.shape[0]
@@ -435,7 +470,7 @@ def moe_dispatch_nvfp4(topk_ids: torch.Tensor, X: torch.Tensor, E: int, sf_block
     _check("gsg_moe_dispatch_nvfp4", lib().gsg_moe_dispatch_nvfp4(
         _ptr(topk_ids), _ptr(X), T, k, E, K, sf_block, _ptr(x_scale_in), _ptr(out_route.offsets),
         _ptr(out_route.perm_src), _ptr(out_route.inv_perm), _ptr(out_act.codes), _ptr(out_act.scales),
-        _ptr(out_act.x_scale), _ptr(ws), ws.numel(), _stream(stream)))
+        _ptr(out_act.x_scale), _ptr(ws), ws.numel(), _stream()))
     return out_route, out_act
 
 
@@ -443,6 +478,8 @@ def grouped_sparse_gemm(act: QuantizedActivations, w: PackedSparseWeights, offse
                         max_rows_per_expert: int = -1, out: Optional[torch.Tensor] = None,
                         out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """Y [R, N] = per-expert X_e . W_e^T on paired 4:8 NVFP4 weights (gsg_grouped_sparse_gemm)."""
+    if stream is not None:
+        return _on_stream(grouped_sparse_gemm, stream, act, w, offsets, max_rows_per_expert, out, out_dtype)
     assert act.sf_block == 32 and act.K == w.K
     _need_cuda(act.codes, act.scales, offsets)
     if out is None:
@@ -450,7 +487,7 @@ def grouped_sparse_gemm(act: QuantizedActivations, w: PackedSparseWeights, offse
     ydt = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
     _check("gsg_grouped_sparse_gemm", lib().gsg_grouped_sparse_gemm(
         _ptr(act.codes), _ptr(act.scales), _ptr(act.x_scale), _ptr(w.packed), _ptr(w.w_scale),
-        _ptr(offsets), w.E, w.N, w.K, act.R, max_rows_per_expert, _ptr(out), ydt, _stream(stream)))
+        _ptr(offsets), w.E, w.N, w.K, act.R, max_rows_per_expert, _ptr(out), ydt, _stream()))
     return out
 
 
@@ -460,6 +497,8 @@ def grouped_sparse_gemm_swiglu(act: QuantizedActivations, w: PackedSparseWeights
     """Up-projection (fused gate|up weights [2I, K]) with SwiGLU and NVFP4 quantization of
     h = silu(gate) * up in the epilogue (gsg_grouped_sparse_gemm_swiglu): returns h's codes and
     scales, ready as the down-projection's activations (tensor scale h_scale, fp32 [1])."""
+    if stream is not None:
+        return _on_stream(grouped_sparse_gemm_swiglu, stream, act, w, offsets, h_scale, max_rows_per_expert, out)
     assert act.sf_block == 32 and act.K == w.K and w.N % 256 == 0
     _need_cuda(act.codes, act.scales, offsets, h_scale)
     I = w.N // 2
@@ -471,7 +510,7 @@ def grouped_sparse_gemm_swiglu(act: QuantizedActivations, w: PackedSparseWeights
     _check("gsg_grouped_sparse_gemm_swiglu", lib().gsg_grouped_sparse_gemm_swiglu(
         _ptr(act.codes), _ptr(act.scales), _ptr(act.x_scale), _ptr(w.packed), _ptr(w.w_scale),
         _ptr(offsets), w.E, w.N, w.K, act.R, max_rows_per_expert, _ptr(h_scale), _ptr(out.codes),
-        _ptr(out.scales), _stream(stream)))
+        _ptr(out.scales), _stream()))
     return out
 
 
@@ -486,6 +525,9 @@ def grouped_sparse_gemm_combine(act: QuantizedActivations, w: PackedSparseWeight
     """Down-projection with the gate-weighted combine fused into the epilogue
     (gsg_grouped_sparse_gemm_combine): out [T, N] bf16, bit for bit grouped_sparse_gemm followed by
     unpermute_scale.  workspace from combine_workspace (zero before the first call, left zero)."""
+    if stream is not None:
+        return _on_stream(grouped_sparse_gemm_combine, stream, act, w, routing, gates, workspace, max_rows_per_expert,
+                          out)
     assert act.sf_block == 32 and act.K == w.K and act.R == routing.T * routing.k
     _need_cuda(act.codes, act.scales, routing.offsets, routing.perm_src, gates, workspace)
     T, k = routing.T, routing.k
@@ -494,7 +536,7 @@ def grouped_sparse_gemm_combine(act: QuantizedActivations, w: PackedSparseWeight
     _check("gsg_grouped_sparse_gemm_combine", lib().gsg_grouped_sparse_gemm_combine(
         _ptr(act.codes), _ptr(act.scales), _ptr(act.x_scale), _ptr(w.packed), _ptr(w.w_scale),
         _ptr(routing.offsets), w.E, w.N, w.K, T, k, max_rows_per_expert, _ptr(routing.perm_src), _ptr(gates),
-        _ptr(workspace), workspace.numel(), _ptr(out), _stream(stream)))
+        _ptr(workspace), workspace.numel(), _ptr(out), _stream()))
     return out
 
 
@@ -502,6 +544,8 @@ def grouped_dense_gemm(act: QuantizedActivations, w: PackedDenseWeights, offsets
                        max_rows_per_expert: int = -1, out: Optional[torch.Tensor] = None,
                        out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """Dense-NVFP4 control on the same skeleton (gsg_grouped_dense_gemm)."""
+    if stream is not None:
+        return _on_stream(grouped_dense_gemm, stream, act, w, offsets, max_rows_per_expert, out, out_dtype)
     assert act.sf_block == 16 and act.K == w.K
     _need_cuda(act.codes, act.scales, offsets)
     if out is None:
@@ -509,7 +553,7 @@ def grouped_dense_gemm(act: QuantizedActivations, w: PackedDenseWeights, offsets
     ydt = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
     _check("gsg_grouped_dense_gemm", lib().gsg_grouped_dense_gemm(
         _ptr(act.codes), _ptr(act.scales), _ptr(act.x_scale), _ptr(w.packed), _ptr(w.w_scale),
-        _ptr(offsets), w.E, w.N, w.K, act.R, max_rows_per_expert, _ptr(out), ydt, _stream(stream)))
+        _ptr(offsets), w.E, w.N, w.K, act.R, max_rows_per_expert, _ptr(out), ydt, _stream()))
     return out
 
 
@@ -518,6 +562,8 @@ def grouped_dense_gemm_native(act: QuantizedActivations, w: PackedDenseWeights, 
                               out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """The dense-NVFP4 control with the token rows as MMA operand A (the activation-stationary
     orientation, gsg_grouped_dense_gemm_native); the same result as grouped_dense_gemm."""
+    if stream is not None:
+        return _on_stream(grouped_dense_gemm_native, stream, act, w, offsets, max_rows_per_expert, out, out_dtype)
     assert act.sf_block == 16 and act.K == w.K
     _need_cuda(act.codes, act.scales, offsets)
     if out is None:
@@ -525,14 +571,14 @@ def grouped_dense_gemm_native(act: QuantizedActivations, w: PackedDenseWeights, 
     ydt = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
     _check("gsg_grouped_dense_gemm_native", lib().gsg_grouped_dense_gemm_native(
         _ptr(act.codes), _ptr(act.scales), _ptr(act.x_scale), _ptr(w.packed), _ptr(w.w_scale),
-        _ptr(offsets), w.E, w.N, w.K, act.R, max_rows_per_expert, _ptr(out), ydt, _stream(stream)))
+        _ptr(offsets), w.E, w.N, w.K, act.R, max_rows_per_expert, _ptr(out), ydt, _stream()))
     return out
 
 
 # ------------------------------------------------------------------ router, norm, microscaled experts
-def _args(stream, *ts: Optional[torch.Tensor]) -> int:
+def _args(*ts: Optional[torch.Tensor]) -> int:
     """The checks of the tensors of one call (CUDA, contiguous, on the current device, where the kernels
-    run) and the stream to launch on."""
+    run) and the current stream, to launch on."""
     dev = torch.cuda.current_device()
     for t in ts:
         if t is not None and (t.get_device() != dev or not t.is_contiguous()):
@@ -542,7 +588,7 @@ def _args(stream, *ts: Optional[torch.Tensor]) -> int:
                 raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is cuda:{dev}")
             raise ValueError("tensors must be contiguous")
     # (the raw handle: building a Stream object takes 3 us, as long as the rest of a small call)
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _new(rows: int, cols: int, dtype, device) -> torch.Tensor:
@@ -592,6 +638,9 @@ def moe_gate(logits: torch.Tensor, top_k: int, scoring: str = "softmax", bias: O
              out_ids: Optional[torch.Tensor] = None, out_gates: Optional[torch.Tensor] = None, stream=None):
     """Router logits bf16 or fp32 [T, E] -> (topk ids int32 [T, top_k], gates fp32 [T, top_k]), as the routing
     calls and unpermute_scale take them (gsg_moe_gate)."""
+    if stream is not None:
+        return _on_stream(moe_gate, stream, logits, top_k, scoring, bias, n_group, topk_group, group_top, renormalize,
+                          scale, out_ids, out_gates)
     if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"logits: fp32 or bf16 [T, E] wanted, got {logits.dtype} {tuple(logits.shape)}")
     if scoring not in _SCORES:
@@ -599,7 +648,7 @@ def moe_gate(logits: torch.Tensor, top_k: int, scoring: str = "softmax", bias: O
     T, E = logits.shape
     if bias is not None and (bias.dtype != torch.float32 or bias.numel() != E):
         raise ValueError(f"bias: fp32 of {E} entries wanted")
-    s = _args(stream, logits, bias, out_ids, out_gates)
+    s = _args(logits, bias, out_ids, out_gates)
     if out_ids is None:
         out_ids = _new(T, top_k, torch.int32, logits.device)
     else:
@@ -622,12 +671,14 @@ def add_rmsnorm_mx(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     """h = x + residual, y = rmsnorm(h) * weight; y in bf16 (want_y) and in MXFP8 or MXFP4 (fmt, None: not)
     from one pass (gsg_add_rmsnorm_mx).  x bf16 [T, K], residual bf16 or fp32 (out_h may be the residual
     itself), weight bf16 or fp32 [K]."""
+    if stream is not None:
+        return _on_stream(add_rmsnorm_mx, stream, x, weight, residual, eps, fmt, want_y, out_act, out_y, out_h)
     if x.dim() != 2 or x.dtype != torch.bfloat16:
         raise ValueError(f"x: bf16 [T, K] wanted, got {x.dtype} {tuple(x.shape)}")
     T, K = x.shape
     if weight.numel() != K or weight.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"weight: fp32 or bf16 of {K} entries wanted")
-    s = _args(stream, x, weight, residual, out_y, out_h, None if out_act is None else out_act.codes,
+    s = _args(x, weight, residual, out_y, out_h, None if out_act is None else out_act.codes,
               None if out_act is None else out_act.scales)
     h = y = act = None
     if residual is not None:
@@ -648,10 +699,12 @@ def add_rmsnorm_mx(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
 
 def pack_mxfp4(W: torch.Tensor, out: Optional[PackedMxWeights] = None, stream=None) -> PackedMxWeights:
     """W fp32 or bf16 [E, N, K] -> MXFP4 packed weights (gsg_pack_mxfp4)."""
+    if stream is not None:
+        return _on_stream(pack_mxfp4, stream, W, out)
     if W.dim() != 3 or W.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"W: fp32 or bf16 [E, N, K] wanted, got {W.dtype} {tuple(W.shape)}")
     E, N, K = W.shape
-    s = _args(stream, W, None if out is None else out.packed)
+    s = _args(W, None if out is None else out.packed)
     out = _mx_weights(out, E, N, K, W)
     _check("gsg_pack_mxfp4", lib().gsg_pack_mxfp4(
         W.data_ptr(), OUT_F32 if W.dtype == torch.float32 else OUT_BF16, E, N, K, out.packed.data_ptr(), s))
@@ -662,12 +715,14 @@ def pack_mxfp4_codes(codes: torch.Tensor, scales: torch.Tensor, out: Optional[Pa
                      stream=None) -> PackedMxWeights:
     """MXFP4 weights as checkpoints store them (codes uint8 [E, N, K/2], low nibble = even k; scale bytes
     uint8 [E, N, K/32]) -> packed weights, values unchanged (gsg_pack_mxfp4_codes)."""
+    if stream is not None:
+        return _on_stream(pack_mxfp4_codes, stream, codes, scales, out)
     if codes.dim() != 3 or codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
         raise ValueError("codes uint8 [E, N, K/2] and scales uint8 [E, N, K/32] wanted")
     E, N, K = codes.shape[0], codes.shape[1], codes.shape[2] * 2
     if tuple(scales.shape) != (E, N, K // 32):
         raise ValueError(f"scales: {tuple(scales.shape)}, expected {(E, N, K // 32)}")
-    s = _args(stream, codes, scales, None if out is None else out.packed)
+    s = _args(codes, scales, None if out is None else out.packed)
     out = _mx_weights(out, E, N, K, codes)
     _check("gsg_pack_mxfp4_codes", lib().gsg_pack_mxfp4_codes(
         codes.data_ptr(), scales.data_ptr(), E, N, K, out.packed.data_ptr(), s))
@@ -678,12 +733,14 @@ def quantize_act_mx(X: torch.Tensor, fmt: int = MXFP8, inv_perm: Optional[torch.
                     out: Optional[MxActivations] = None, workspace: Optional[torch.Tensor] = None,
                     stream=None) -> MxActivations:
     """X bf16 [T, K] -> MXFP4 or MXFP8 codes and scales in routed row order (gsg_quantize_act_mx)."""
+    if stream is not None:
+        return _on_stream(quantize_act_mx, stream, X, fmt, inv_perm, top_k, out, workspace)
     if X.dim() != 2 or X.dtype != torch.bfloat16:
         raise ValueError(f"X: bf16 [T, K] wanted, got {X.dtype} {tuple(X.shape)}")
     T, K = X.shape
     if inv_perm is not None and (inv_perm.dtype != torch.int32 or inv_perm.numel() < T * top_k):
         raise ValueError(f"inv_perm: int32 of {T * top_k} entries wanted")
-    s = _args(stream, X, inv_perm, workspace, None if out is None else out.codes, None if out is None else out.scales)
+    s = _args(X, inv_perm, workspace, None if out is None else out.codes, None if out is None else out.scales)
     out = _mx_activations(out, T * top_k, K, fmt, X)
     L = lib()
     if workspace is None and T * top_k * K >= 1 << 26:   # (below that the call needs none)
@@ -699,6 +756,8 @@ def grouped_mx_gemm(act: MxActivations, w: PackedMxWeights, offsets: torch.Tenso
                     stream=None) -> torch.Tensor:
     """Y [R, N] = per-expert X_e . W_e^T on MXFP4 weights, MXFP4 or MXFP8 activations
     (gsg_grouped_mx_gemm).  One expert with offsets [0, R] is a plain linear layer."""
+    if stream is not None:
+        return _on_stream(grouped_mx_gemm, stream, act, w, offsets, max_rows_per_expert, out, out_dtype)
     if act.K != w.K:
         raise ValueError(f"activations have K = {act.K}, weights K = {w.K}")
     if offsets.dtype != torch.int32 or offsets.numel() != w.E + 1:
@@ -712,7 +771,7 @@ def grouped_mx_gemm(act: MxActivations, w: PackedMxWeights, offsets: torch.Tenso
         out_dtype = out.dtype
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"out: bf16 or fp32, got {out_dtype}")
-    s = _args(stream, act.codes, act.scales, w.packed, offsets, out)
+    s = _args(act.codes, act.scales, w.packed, offsets, out)
     if out is None:
         out = _new(act.R, w.N, out_dtype, act.codes.device)
     else:
@@ -726,6 +785,8 @@ def grouped_mx_gemm(act: MxActivations, w: PackedMxWeights, offsets: torch.Tenso
 def unpermute_scale(Y: torch.Tensor, inv_perm: torch.Tensor, gates: torch.Tensor, top_k: int,
                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """out[t] = bf16(sum_j gates[t, j] * Y[inv_perm[t*k + j]]) (gsg_unpermute_scale)."""
+    if stream is not None:
+        return _on_stream(unpermute_scale, stream, Y, inv_perm, gates, top_k, out)
     _need_cuda(Y, inv_perm, gates)
     assert Y.dtype == torch.bfloat16 and gates.dtype == torch.float32
     T = gates.shape[0]
@@ -733,7 +794,7 @@ def unpermute_scale(Y: torch.Tensor, inv_perm: torch.Tensor, gates: torch.Tensor
     if out is None:
         out = torch.empty(T, N, dtype=torch.bfloat16, device=Y.device)
     _check("gsg_unpermute_scale", lib().gsg_unpermute_scale(
-        _ptr(Y), _ptr(inv_perm), _ptr(gates), T, top_k, N, _ptr(out), _stream(stream)))
+        _ptr(Y), _ptr(inv_perm), _ptr(gates), T, top_k, N, _ptr(out), _stream()))
     return out
 
 
