@@ -285,11 +285,12 @@ __device__ __forceinline__ void tc_mma_dense_pair(uint32_t d, uint64_t adesc, ui
 __host__ __device__ constexpr uint32_t idesc_sf(int sf) { return ((uint32_t)sf << 4) | ((uint32_t)sf << 29); }
 
 // The four MMAs of a microscaled chunk (dense, one UE8M0 scale per 32 values): 4-bit weights against 4-bit
-// (kM8 false, K = 64 each) or 8-bit activations (K = 32), for one CTA or a CTA pair.  Each takes the next 32 bytes of the operands' rows; idesc names the bytes of the scale words used
-// (see idesc_sf): with 8-bit activations one word holds all four MMAs' scales, else two words (four columns
-// each, kSfbStep for the tokens') two each.  `accumulate` is for the first of them.  (One election for the four:
-// a stage's issue bounds short tiles; 30B down-projection decode, 8-bit, 26.8 -> 25.8 us.  A predicate from a
-// register in place of elect.sync: 33.6 us.)
+// (kM8 false, K = 64 each) or 8-bit activations (K = 32), for one CTA or a CTA pair.  Each takes the next 32
+// bytes of the operands' rows; idesc names the bytes of the scale words used (see idesc_sf): with 8-bit
+// activations one word holds all four MMAs' scales, else two words (four columns each, kSfbStep for the
+// tokens') two each.  `accumulate` is for the first of them.  (One election for the four: a stage's issue
+// bounds short tiles; 30B down-projection decode, 8-bit, 26.8 -> 25.8 us.  A predicate from a register in place
+// of elect.sync: 33.6 us.)
 template <bool kM8, bool kPair, int kSfbStep>
 __device__ __forceinline__ void tc_mma_mx_chunk(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                 uint32_t accumulate, uint32_t sfa, uint32_t sfb) {
@@ -1140,34 +1141,34 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
             }
         } else {
 #pragma unroll
-        for (int ch = 0; ch < G::kCPS; ++ch) {
-          if (ch < nch) {
+          for (int ch = 0; ch < G::kCPS; ++ch) {
+            if (ch < nch) {
 #pragma unroll
-            for (int h = 0; h < G::kKbPerChunk; ++h) {
-              const int kbi = ch * G::kSfPerChunk + h;   // scale atom
-              const uint64_t bdesc = smem_desc(st + ch * G::kBChunk + G::kBStep * h, 16, 1024, 2);
-              const uint32_t accum = (kc | ch | h) != 0 ? 1u : 0u;
+              for (int h = 0; h < G::kKbPerChunk; ++h) {
+                const int kbi = ch * G::kSfPerChunk + h;   // scale atom
+                const uint64_t bdesc = smem_desc(st + ch * G::kBChunk + G::kBStep * h, 16, 1024, 2);
+                const uint32_t accum = (kc | ch | h) != 0 ? 1u : 0u;
 #pragma unroll
-              for (int t = 0; t < G::kNT; ++t) {
-                const uint32_t aaddr = st + G::kOffW + (t * G::kCPS + ch) * G::kCB + 4096u * h;
-                const uint64_t adesc = smem_desc(aaddr, 128, 256, 0);
-                const uint32_t d = d_tmem + (uint32_t)(t * G::kAccStride);
-                const int kt = t * G::kSfps + kbi;
-                const uint32_t sfa = tset + G::kColSFA + 4 * kt, sfb = tset + G::kColSFB + 4 * kbi;
-                if constexpr (kNative)   // tokens as A, weights as B: the operands and their scales swap
-                  tc_mma_dense(d, bdesc, adesc, idesc, accum, sfb, sfa);
-                else if constexpr (kSparse && kPair)
-                  tc_mma_sparse_pair(d, adesc, bdesc, idesc, accum, sfa, sfb, tset + 2 * kt);
-                else if constexpr (kSparse)
-                  tc_mma_sparse(d, adesc, bdesc, idesc, accum, sfa, sfb, tset + 2 * kt);
-                else if constexpr (kPair)
-                  tc_mma_dense_pair(d, adesc, bdesc, idesc, accum, sfa, sfb);
-                else
-                  tc_mma_dense(d, adesc, bdesc, idesc, accum, sfa, sfb);
+                for (int t = 0; t < G::kNT; ++t) {
+                  const uint32_t aaddr = st + G::kOffW + (t * G::kCPS + ch) * G::kCB + 4096u * h;
+                  const uint64_t adesc = smem_desc(aaddr, 128, 256, 0);
+                  const uint32_t d = d_tmem + (uint32_t)(t * G::kAccStride);
+                  const int kt = t * G::kSfps + kbi;
+                  const uint32_t sfa = tset + G::kColSFA + 4 * kt, sfb = tset + G::kColSFB + 4 * kbi;
+                  if constexpr (kNative)   // tokens as A, weights as B: the operands and their scales swap
+                    tc_mma_dense(d, bdesc, adesc, idesc, accum, sfb, sfa);
+                  else if constexpr (kSparse && kPair)
+                    tc_mma_sparse_pair(d, adesc, bdesc, idesc, accum, sfa, sfb, tset + 2 * kt);
+                  else if constexpr (kSparse)
+                    tc_mma_sparse(d, adesc, bdesc, idesc, accum, sfa, sfb, tset + 2 * kt);
+                  else if constexpr (kPair)
+                    tc_mma_dense_pair(d, adesc, bdesc, idesc, accum, sfa, sfb);
+                  else
+                    tc_mma_dense(d, adesc, bdesc, idesc, accum, sfa, sfb);
+                }
               }
             }
           }
-        }
         }
         if constexpr (kPair) tc_commit_pair(empty_bar(s), 3);   // the stage is free in both CTAs
         else tc_commit(empty_bar(s));
@@ -1369,64 +1370,65 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
       }
       const bool direct = kBN >= 128 && G::kNT == 1 + (kWide ? 1 : 0) && !p.y_f32 && p.perm_src == nullptr;
       for (int u = u_begin; u < u_end && !direct; ++u) {
-
-      // first feature of this warp
-      const size_t col0 = ((size_t)c.nt * kCG * G::kNT + u * kCG + rank) * kTileN + 32 * q;
-      for (int c0 = 0; c0 < valid; c0 += 16) {
-        float v[16];
-        tc_ld_16(taddr + (uint32_t)(u * G::kAccStride) + c0, v);
-        if (p.y_f32) {
+        // first feature of this warp
+        const size_t col0 = ((size_t)c.nt * kCG * G::kNT + u * kCG + rank) * kTileN + 32 * q;
+        for (int c0 = 0; c0 < valid; c0 += 16) {
+          float v[16];
+          tc_ld_16(taddr + (uint32_t)(u * G::kAccStride) + c0, v);
+          if (p.y_f32) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(obuf_s + (uint32_t)(j * 128 + lane * 4)), "f"(__fmul_rn(v[j], scale)) : "memory");
-          __syncwarp();
-          float* Y = static_cast<float*>(p.Y);
+            for (int j = 0; j < 16; ++j)
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(obuf_s + (uint32_t)(j * 128 + lane * 4)),
+                           "f"(__fmul_rn(v[j], scale)) : "memory");
+            __syncwarp();
+            float* Y = static_cast<float*>(p.Y);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {          // 16 tokens x 8 chunks of 16 B
-            const int ci = lane + 32 * k, tok = ci >> 3, part = ci & 7;
-            if (c0 + tok < valid) {
-              uint32_t a, b, cc, d;
-              lds128(obuf_s + (uint32_t)(tok * 128 + part * 16), a, b, cc, d);
-              *reinterpret_cast<uint4*>(Y + (size_t)(r0 + c0 + tok) * p.N + col0 + part * 4) = make_uint4(a, b, cc, d);
+            for (int k = 0; k < 4; ++k) {          // 16 tokens x 8 chunks of 16 B
+              const int ci = lane + 32 * k, tok = ci >> 3, part = ci & 7;
+              if (c0 + tok < valid) {
+                uint32_t a, b, cc, d;
+                lds128(obuf_s + (uint32_t)(tok * 128 + part * 16), a, b, cc, d);
+                *reinterpret_cast<uint4*>(Y + (size_t)(r0 + c0 + tok) * p.N + col0 + part * 4) =
+                    make_uint4(a, b, cc, d);
+              }
+            }
+          } else if constexpr (kMx) {
+            uint32_t h8[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h8[j] = pack_bf16<false>(v[2 * j], v[2 * j + 1], 1.0f);
+            store_pairs<8>(static_cast<__nv_bfloat16*>(p.Y) + (size_t)(r0 + c0 + (lane & 1)) * p.N + col0 + (lane & ~1),
+                           (size_t)p.N, valid - c0, lane, h8);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const unsigned short h = __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(v[j], scale)));
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(obuf_s + (uint32_t)(j * 64 + lane * 2)), "h"(h) : "memory");
+            }
+            __syncwarp();
+            __nv_bfloat16* Y = static_cast<__nv_bfloat16*>(p.Y);
+            // combine: lane j < 16 holds the flat index f = t*k + j of chunk row j; the row goes to
+            // slot f instead of row r
+            const bool comb = p.perm_src != nullptr;
+            int myf = (comb && lane < 16 && c0 + lane < valid) ? __ldg(p.perm_src + r0 + c0 + lane) : 0;
+            // a slot index outside [0, T*k) (corrupt routing) gets nothing stored
+            const unsigned badf = __ballot_sync(0xffffffffu, comb && lane < 16 && c0 + lane < valid &&
+                                                                 (myf < 0 || myf >= p.R));
+            if (badf != 0u && lane == 0) set_status(p.status, GSG_ERR_BAD_ROUTING);
+            if ((badf >> lane) & 1u) myf = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {          // 16 tokens x 4 chunks of 16 B
+              const int ci = lane + 32 * k, tok = ci >> 2, part = ci & 3;
+              const int f = __shfl_sync(0xffffffffu, myf, tok);
+              if (c0 + tok < valid && !((badf >> tok) & 1u)) {
+                uint32_t a, b, cc, d;
+                lds128(obuf_s + (uint32_t)(tok * 64 + part * 16), a, b, cc, d);
+                const size_t dst = comb ? (size_t)f : (size_t)(r0 + c0 + tok);
+                *reinterpret_cast<uint4*>(Y + dst * p.N + col0 + part * 8) = make_uint4(a, b, cc, d);
+              }
             }
           }
-        } else if constexpr (kMx) {
-          uint32_t h8[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) h8[j] = pack_bf16<false>(v[2 * j], v[2 * j + 1], 1.0f);
-          store_pairs<8>(static_cast<__nv_bfloat16*>(p.Y) + (size_t)(r0 + c0 + (lane & 1)) * p.N + col0 + (lane & ~1),
-                         (size_t)p.N, valid - c0, lane, h8);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const unsigned short h = __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(v[j], scale)));
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(obuf_s + (uint32_t)(j * 64 + lane * 2)), "h"(h) : "memory");
-          }
           __syncwarp();
-          __nv_bfloat16* Y = static_cast<__nv_bfloat16*>(p.Y);
-          // combine: lane j < 16 holds the flat index f = t*k + j of chunk row j; the row goes to
-          // slot f instead of row r
-          const bool comb = p.perm_src != nullptr;
-          int myf = (comb && lane < 16 && c0 + lane < valid) ? __ldg(p.perm_src + r0 + c0 + lane) : 0;
-          // a slot index outside [0, T*k) (corrupt routing) gets nothing stored
-          const unsigned badf = __ballot_sync(0xffffffffu, comb && lane < 16 && c0 + lane < valid &&
-                                                               (myf < 0 || myf >= p.R));
-          if (badf != 0u && lane == 0) set_status(p.status, GSG_ERR_BAD_ROUTING);
-          if ((badf >> lane) & 1u) myf = 0;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {          // 16 tokens x 4 chunks of 16 B
-            const int ci = lane + 32 * k, tok = ci >> 2, part = ci & 3;
-            const int f = __shfl_sync(0xffffffffu, myf, tok);
-            if (c0 + tok < valid && !((badf >> tok) & 1u)) {
-              uint32_t a, b, cc, d;
-              lds128(obuf_s + (uint32_t)(tok * 64 + part * 16), a, b, cc, d);
-              const size_t dst = comb ? (size_t)f : (size_t)(r0 + c0 + tok);
-              *reinterpret_cast<uint4*>(Y + dst * p.N + col0 + part * 8) = make_uint4(a, b, cc, d);
-            }
-          }
         }
-        __syncwarp();
-      }
       }
       }
       if (!released) {
