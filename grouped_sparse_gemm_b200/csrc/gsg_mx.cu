@@ -111,8 +111,8 @@ cudaError_t launch_pack_mxfp4_codes(const uint8_t* codes, const uint8_t* scales,
 // ------------------------------------------------------------------ activation quantizer + dispatch
 // A lane makes 16 bytes of codes: a whole 32-block in 4 bits, half of one in 8 bits (two lanes share the
 // block's maximum).  Every token is read and quantized once and written to its k routed rows.  Bound by the scattered
-// scale words' sectors and the codes' writes: 512 tokens x 8 rows x 2048, 4-bit, 4.5 us; 1023 rows x 7168, 8-bit,
-// 5.6 us; 1368 tokens x 8 x 7168, 4-bit, 18 us (3.4 TB/s of what it has to move).
+// scale words' sectors and the codes' writes.  Alone, in a graph of calls on buffers that change: 512 tokens x 8 rows x
+// 2048, 4-bit, 3.8 us; 1023 rows x 7168, 8-bit, 6.4 us; 1368 tokens x 8 x 7168, 4-bit, 20.7 us.
 struct MxQuantParams {
   const uint16_t* X;
   const int32_t* inv_perm;
@@ -216,14 +216,21 @@ size_t quant_mx_raw_bytes(long long R, int K, int k) {
   return R * (long long)K >= (k > 1 ? 1ll << 26 : 1ll << 27) ? (size_t)(R * (long long)(K / 128) * 4) : 0;
 }
 
-constexpr int kMxSpreadSmem = 220 * 1024;   // an SM's shared memory, less the blocks' reserved parts
+constexpr int kSmSharedBytes = 228 * 1024;   // an SM's shared memory, of which every block takes 1 KB beside its own
+// Shared memory with which an SM holds `fair` blocks and not one more.
+constexpr int mx_spread_smem(int fair) { return kSmSharedBytes / (fair + 1); }
+constexpr bool mx_spread_holds(int fair, int blocks) {
+  return blocks * (mx_spread_smem(fair) + 1024) <= kSmSharedBytes;
+}
+static_assert(mx_spread_holds(1, 1) && !mx_spread_holds(1, 2) && mx_spread_holds(2, 2) && !mx_spread_holds(2, 3) &&
+              mx_spread_holds(3, 3) && !mx_spread_holds(3, 4), "blocks per SM");
 
 cudaError_t quant_mx_set_smem_attrs() {
   cudaError_t e = cudaFuncSetAttribute(act_quant_mx_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kMxSpreadSmem / 2 + 1024);
+                                       mx_spread_smem(1));
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(act_quant_mx_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMxSpreadSmem / 2 + 1024);
+                             mx_spread_smem(1));
   return e;
 }
 
@@ -237,9 +244,10 @@ cudaError_t launch_quant_mx(const uint16_t* X, int T, int K, int bits, const int
   if (blocks > (long long)num_sms * 16) blocks = (long long)num_sms * 16;
   // Launched early, behind a GEMM that fills the SMs, the blocks of a small grid would all settle on the first
   // SMs to come free and share them (measured: 4096 rows x 2048, quantizer + product 53.4 us instead of 45.3).
-  // The shared memory that each asks for, and does not use, leaves room for its fair number per SM only.
+  // The shared memory that each asks for, and does not use, leaves room for its fair number per SM only.  (With room
+  // for one more: 4096 rows x 2048 46.6 us instead of 45.8, the quantizer alone 4.9 instead of 3.8.)
   const long long fair = (blocks + num_sms - 1) / num_sms;
-  const size_t smem = fair < 4 ? (size_t)kMxSpreadSmem / (size_t)(fair + 1) + 1024 : 0;
+  const size_t smem = fair < 4 ? (size_t)mx_spread_smem((int)fair) : 0;
   const cudaError_t e = bits == 8
       ? launch_pdl(act_quant_mx_kernel<8>, (unsigned)blocks, kMxQuantThreads, smem, stream, p)
       : launch_pdl(act_quant_mx_kernel<4>, (unsigned)blocks, kMxQuantThreads, smem, stream, p);
