@@ -678,6 +678,10 @@ def add_rmsnorm_mx(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     T, K = x.shape
     if weight.numel() != K or weight.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"weight: fp32 or bf16 of {K} entries wanted")
+    if out_h is not None and residual is None:
+        raise ValueError("out_h: without a residual there is no h to write")
+    if out_act is not None and fmt is None:
+        raise ValueError("out_act: without a fmt there are no codes to write")
     s = _args(x, weight, residual, out_y, out_h, None if out_act is None else out_act.codes,
               None if out_act is None else out_act.scales)
     h = y = act = None
