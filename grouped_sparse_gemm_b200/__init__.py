@@ -596,6 +596,10 @@ def _new(rows: int, cols: int, dtype, device) -> torch.Tensor:
     return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
+def _too_long(what: str) -> ValueError:
+    return ValueError(f"{what}: the library's sizes have 31 bits")
+
+
 def _check_out(t: torch.Tensor, shape, dtype, what: str) -> torch.Tensor:
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} {dtype}")
@@ -646,6 +650,8 @@ def moe_gate(logits: torch.Tensor, top_k: int, scoring: str = "softmax", bias: O
     if scoring not in _SCORES:
         raise ValueError(f"scoring {scoring!r}: 'softmax' or 'sigmoid'")
     T, E = logits.shape
+    if (T | top_k | n_group | topk_group | group_top) >> 31:   # (ctypes would keep the low 32 bits)
+        raise _too_long(f"{T} tokens, top_k {top_k}, groups {n_group}, {topk_group}, {group_top}")
     if bias is not None and (bias.dtype != torch.float32 or bias.numel() != E):
         raise ValueError(f"bias: fp32 of {E} entries wanted")
     s = _args(logits, bias, out_ids, out_gates)
@@ -676,6 +682,8 @@ def add_rmsnorm_mx(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     if x.dim() != 2 or x.dtype != torch.bfloat16:
         raise ValueError(f"x: bf16 [T, K] wanted, got {x.dtype} {tuple(x.shape)}")
     T, K = x.shape
+    if T >> 31:
+        raise _too_long(f"{T} tokens")
     if weight.numel() != K or weight.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"weight: fp32 or bf16 of {K} entries wanted")
     if out_h is not None and residual is None:
@@ -742,6 +750,8 @@ def quantize_act_mx(X: torch.Tensor, fmt: int = MXFP8, inv_perm: Optional[torch.
     if X.dim() != 2 or X.dtype != torch.bfloat16:
         raise ValueError(f"X: bf16 [T, K] wanted, got {X.dtype} {tuple(X.shape)}")
     T, K = X.shape
+    if (T | top_k) >> 31:
+        raise _too_long(f"{T} tokens, top_k {top_k}")
     if inv_perm is not None and (inv_perm.dtype != torch.int32 or inv_perm.numel() < T * top_k):
         raise ValueError(f"inv_perm: int32 of {T * top_k} entries wanted")
     s = _args(X, inv_perm, workspace, None if out is None else out.codes, None if out is None else out.scales)
