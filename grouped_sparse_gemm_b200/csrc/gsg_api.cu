@@ -47,6 +47,7 @@ gsg_status_t device_state(DeviceState** out) {
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool aligned128(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 127u) == 0; }
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 inline gsg_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? GSG_OK : GSG_ERR_CUDA; }
@@ -265,7 +266,7 @@ gsg_status_t gsg_quantize_act_mx(const uint16_t* X, int T, int K, int fmt, const
   if (inv_perm == nullptr && k != 1) return GSG_ERR_INVALID_ARG;
   if (T == 0) return GSG_OK;
   if (!X || !codes || !scales) return GSG_ERR_INVALID_ARG;
-  if (!aligned16(X) || !aligned16(codes) || !aligned16(scales)) return GSG_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(codes) || !aligned16(scales) || !aligned4(inv_perm)) return GSG_ERR_INVALID_ARG;
   const size_t need = gsg_workspace_size(GSG_OP_QUANTIZE_MX, 0, 0, K, T, k);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))) return GSG_ERR_WORKSPACE;
   DeviceState* d = nullptr;
@@ -288,6 +289,9 @@ gsg_status_t gsg_moe_gate(const void* logits, int logits_dtype, const float* bia
     return GSG_ERR_INVALID_ARG;
   if (T == 0) return GSG_OK;
   if (!logits || !topk_ids || !gates) return GSG_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(logits) & (logits_dtype == GSG_OUT_F32 ? 3u : 1u)) != 0 || !aligned4(bias) ||
+      !aligned4(topk_ids) || !aligned4(gates))
+    return GSG_ERR_INVALID_ARG;
   DeviceState* d = nullptr;
   gsg_status_t st = device_state(&d);
   if (st != GSG_OK) return st;
@@ -328,7 +332,8 @@ gsg_status_t gsg_grouped_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales
   if (!expert_offsets || !w_packed) return GSG_ERR_INVALID_ARG;
   if (R == 0) return GSG_OK;
   if (!a_codes || !a_scales || !Y) return GSG_ERR_INVALID_ARG;
-  if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned128(w_packed) || !aligned16(Y)) return GSG_ERR_INVALID_ARG;
+  if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned128(w_packed) || !aligned16(Y) || !aligned4(expert_offsets))
+    return GSG_ERR_INVALID_ARG;
   DeviceState* d = nullptr;
   gsg_status_t st = device_state(&d);
   if (st != GSG_OK) return st;

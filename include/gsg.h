@@ -129,7 +129,8 @@ gsg_status_t gsg_pack_dense_nvfp4(const float* W, int E, int N, int K, uint8_t* 
  * `scale`.  Ties go to the lowest index, of groups and of experts.  A token with fewer than k available
  * experts gets the lowest-numbered others with gate 0, so its ids are distinct and in range.
  * E <= 1024, k <= 32, n_group <= 32, else GSG_ERR_UNSUPPORTED_SHAPE; E % n_group == 0, k <= topk_group *
- * E/n_group.  A NaN or +inf logit or bias sets GSG_ERR_NONFINITE (the ids stay in range).  No workspace.
+ * E/n_group.  A NaN or +inf logit or bias sets GSG_ERR_NONFINITE (the ids stay in range).  Pointers aligned to
+ * their elements.  No workspace.
  */
 gsg_status_t gsg_moe_gate(const void* logits, int logits_dtype, const float* bias, int T, int E, int k, int scoring,
                           int n_group, int topk_group, int group_top, int renormalize, float scale,
