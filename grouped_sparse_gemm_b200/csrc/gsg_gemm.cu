@@ -955,9 +955,12 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
       // MMA's N = valid rounded up to 16 that this CTA supplies (rank 1: the upper half)
       const int nh = kPair ? ((c.valid + 15) & ~15) / 2 : kBN;
       const int r0 = c.r0 + (int)rank * nh;
-      const int cnt = min(max(c.valid - (int)rank * nh, 0), nh);
-      // (the leader of a microscaled pair also announces the other CTA's rows)
-      const int cnt1 = kMx && kPair ? min(max(c.valid - nh, 0), nh) : 0;
+      // (The leader of a microscaled pair also announces the other CTA's rows.  At least one, also where the leader's
+      // half holds the whole tile: the pair's barrier has to wait for this warp of the other CTA in every stage.  A
+      // warp that it does not wait for may fall a round of the ring behind, and then misreads a phase's parity.)
+      const int least = kMx && kPair ? 1 : 0;
+      const int cnt = min(max(c.valid - (int)rank * nh, least), nh);
+      const int cnt1 = kMx && kPair ? min(max(c.valid - nh, least), nh) : 0;
       // token rows to fetch: whole 32-row boxes (BN <= 32: one box of BN rows), as few 64-row
       // boxes as possible for the larger tiles -- every TMA instruction costs the issuing warp
       const int rows = (cnt + G::kBoxH - 1) / G::kBoxH * G::kBoxH;
