@@ -1082,15 +1082,15 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
             }
           }
         }
-        if constexpr (kMx) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sempty_bar(s));   // the atoms are in registers
-        }
         tc_st_cols<G::kSetUsed>(tmem + tlane + (uint32_t)set * G::kSetCols, r);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {   // the set (and, for a pair, this CTA's stage) is ready for the MMA issuer
+          // The scale ring's stage is free only now that the stores above have taken the atoms from their registers.
+          // Right after the loads it is not: an arrive does not wait for them, and behind the epilogue's stores they
+          // may still be on their way when the next copy lands (one launch in 1500 of 192-token tiles came out wrong).
+          if constexpr (kMx) mbar_arrive(sempty_bar(s));
           if constexpr (kPair) mbar_arrive_cluster(cluster_addr(tfull_bar(set), 0u));
           else mbar_arrive(tfull_bar(set));
         }

@@ -36,3 +36,27 @@ def test_experts_of_a_few_rows_between_long_ones(gsg, N, fmt):
             rows = rows if len(rows) < 20 else rows[:: len(rows) // 7]
             yr, b = ogemm.gemm_rows(A[rows], omx.dequantize(codes[e], sc[e], 4), 1.0)
             tl.assert_gemm_close(y[torch.from_numpy(rows).to(DEV)], yr, b, f"expert {e}")
+
+
+@pytest.mark.parametrize("fmt,N,mean", [(8, 768, 130), (4, 768, 130), (8, 768, 40)])
+def test_runs_are_bit_identical(gsg, fmt, N, mean):
+    """The same product some thousand times over: scales that arrive late, or that are overwritten while they are
+    still read, show in one launch of many."""
+    E, K = 64, 2304
+    g = torch.Generator(device=DEV).manual_seed(5)
+    counts = (-mean * torch.log(torch.rand(E, generator=g, device=DEV).clamp(min=1e-3))).int()
+    off = torch.cat([counts.new_zeros(1), counts.cumsum(0).int()]).int()
+    R = int(off[-1])
+    codes = torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, device=DEV, generator=g)
+    sc = torch.randint(120, 130, (E, N, K // 32), dtype=torch.uint8, device=DEV, generator=g)
+    w = gsg.pack_mxfp4_codes(codes, sc)
+    x = (torch.randn(R, K, generator=g, device=DEV) * torch.exp2(torch.randint(-3, 4, (R, K // 32), generator=g, device=DEV)
+                                                                 .float()).repeat_interleave(32, 1)).to(torch.bfloat16)
+    a = gsg.quantize_act_mx(x, fmt)
+    want = gsg.grouped_mx_gemm(a, w, off)
+    differ = torch.zeros((), dtype=torch.int64, device=DEV)
+    y = torch.empty_like(want)
+    for _ in range(6000):
+        gsg.grouped_mx_gemm(a, w, off, out=y)
+        differ += (y.view(torch.int16) != want.view(torch.int16)).any()
+    assert int(differ) == 0
