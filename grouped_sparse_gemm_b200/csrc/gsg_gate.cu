@@ -73,11 +73,11 @@ template <typename T>
 __device__ __forceinline__ float load_logit(const void* p, size_t i);
 template <>
 __device__ __forceinline__ float load_logit<float>(const void* p, size_t i) {
-  return __ldg(static_cast<const float*>(p) + i);
+  return __ldca(static_cast<const float*>(p) + i);
 }
 template <>
 __device__ __forceinline__ float load_logit<uint16_t>(const void* p, size_t i) {
-  return bf16_bits_to_f32(__ldg(static_cast<const uint16_t*>(p) + i));
+  return bf16_bits_to_f32(__ldca(static_cast<const uint16_t*>(p) + i));
 }
 
 // The same where lane < left, else the lowest number (a predicated load: a branch costs several times more).
@@ -86,14 +86,14 @@ __device__ __forceinline__ float load_logit_if(const T* p, int lane, int left);
 template <>
 __device__ __forceinline__ float load_logit_if<float>(const float* p, int lane, int left) {
   float v;
-  asm("{\n\t.reg .pred q;\n\tsetp.lt.s32 q, %2, %3;\n\tmov.b32 %0, 0xFF7FFFFF;\n\t@q ld.global.nc.f32 %0, [%1];\n\t}"
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.lt.s32 q, %2, %3;\n\tmov.b32 %0, 0xFF7FFFFF;\n\t@q ld.global.f32 %0, [%1];\n\t}"
       : "=f"(v) : "l"(p), "r"(lane), "r"(left));
   return v;
 }
 template <>
 __device__ __forceinline__ float load_logit_if<uint16_t>(const uint16_t* p, int lane, int left) {
   uint16_t v;
-  asm("{\n\t.reg .pred q;\n\tsetp.lt.s32 q, %2, %3;\n\tmov.b16 %0, 0xFF7F;\n\t@q ld.global.nc.u16 %0, [%1];\n\t}"
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.lt.s32 q, %2, %3;\n\tmov.b16 %0, 0xFF7F;\n\t@q ld.global.u16 %0, [%1];\n\t}"
       : "=h"(v) : "l"(p), "r"(lane), "r"(left));
   return bf16_bits_to_f32(v);
 }

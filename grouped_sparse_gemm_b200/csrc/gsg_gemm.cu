@@ -654,7 +654,7 @@ __device__ void combine_tokens(const GemmParams& p, volatile int* abort_flag) {
 #pragma unroll
         for (int jj = 0; jj < 8; ++jj) {
           const bool in = j0 + jj < p.k;
-          g[jj] = in ? __ldg(p.gates + (size_t)t * p.k + j0 + jj) : 0.0f;
+          g[jj] = in ? __ldca(p.gates + (size_t)t * p.k + j0 + jj) : 0.0f;
           v[jj] = in ? __ldcg(reinterpret_cast<const uint4*>(slots + ((size_t)t * p.k + j0 + jj) * p.N) + c)
                      : make_uint4(0u, 0u, 0u, 0u);
         }
@@ -788,7 +788,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
   // block barriers in all, and every thread works out the totals it needs itself.)
   bool bad = false;
   auto offset_at = [&](int i) {
-    const int v = __ldg(p.off + i);
+    const int v = __ldca(p.off + i);
     if (v < 0 || v > p.R) bad = true;
     return min(max(v, 0), p.R);
   };
@@ -801,7 +801,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
     if (hi < lo) bad = true;
     offs[e] = lo;
     if (e == E - 1) offs[E] = hi;
-    if (!kMx) wsc[e] = __ldg(p.w_scale + e);
+    if (!kMx) wsc[e] = __ldca(p.w_scale + e);
     local += (max(hi - lo, 0) + kBN - 1) / kBN * NTt;
   }
   __shared__ int wsum[kThreads / 32];
@@ -1197,7 +1197,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
     // =============================== epilogue (warps 3..6, and 11..14 for wide tiles -> TMEM lane
     // quadrants 3,0,1,2)
     const int q = warp & 3;
-    const float sx = kMx ? 1.0f : __ldg(p.x_scale);
+    const float sx = kMx ? 1.0f : __ldca(p.x_scale);
     int acc = 0;
     uint32_t aph = 0;
     for (int j = 0; j < n_my; ++j) {
@@ -1245,7 +1245,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
         // fp32; the block is transposed through shared memory so that each lane then owns one
         // token's 32 values: block max, UE4M3 scale and E2M1 codes once per token, 16-byte code
         // stores, scale bytes into the quad layout (k-block nt, position q).
-        const float sh = __ldg(p.h_scale);
+        const float sh = __ldca(p.h_scale);
         const float six_sh = __fmul_rn(6.0f, sh);
         const int f0 = c.nt * kTileN + 32 * q;
         const int hrow = p.N / 4;                 // bytes of h codes per row (N/2 features)
@@ -1412,7 +1412,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_con
             // combine: lane j < 16 holds the flat index f = t*k + j of chunk row j; the row goes to
             // slot f instead of row r
             const bool comb = p.perm_src != nullptr;
-            int myf = (comb && lane < 16 && c0 + lane < valid) ? __ldg(p.perm_src + r0 + c0 + lane) : 0;
+            int myf = (comb && lane < 16 && c0 + lane < valid) ? __ldca(p.perm_src + r0 + c0 + lane) : 0;
             // a slot index outside [0, T*k) (corrupt routing) gets nothing stored
             const unsigned badf = __ballot_sync(0xffffffffu, comb && lane < 16 && c0 + lane < valid &&
                                                                  (myf < 0 || myf >= p.R));

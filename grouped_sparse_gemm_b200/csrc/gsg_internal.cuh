@@ -130,6 +130,12 @@ __device__ __forceinline__ float tensor_scale_from_amax(float amax) {
 // read and write comes after pdl_wait(), so stream order is kept exactly; each kernel lets its
 // own successor launch early with pdl_launch_dependents().  Without a programmatic predecessor
 // (first kernel, other work before it) the wait returns at once.
+// What an earlier kernel may have written is read with ordinary loads (__ldca, or __ldcg where nothing is read
+// twice), never with read-only ones (__ldg, ld.global.nc, a const __restrict__ pointer's): those are for data that
+// stays as it is while the kernel is on the device.  A chain of short kernels is on the device all at once, each
+// waiting in pdl_wait(), and the read-only loads of the last may then find what an earlier kernel's loads had
+// brought into L1 before it was rewritten (layers of 16 and 64 tokens, run in a row on one set of buffers, came out
+// wrong).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -207,7 +213,7 @@ __device__ __forceinline__ void block_amax_partial(const uint16_t* __restrict__ 
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const long long i = i0 + u * stride;
-      v[u] = i < n8 ? __ldg(X4 + i) : make_uint4(0u, 0u, 0u, 0u);
+      v[u] = i < n8 ? __ldca(X4 + i) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {

@@ -31,14 +31,14 @@ pack_mxfp4_kernel(const void* __restrict__ W, long long blocks, int N, int K, ui
       const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(W) + i * 32);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float4 x = __ldg(src + j);
+        const float4 x = __ldca(src + j);
         v[4 * j] = x.x; v[4 * j + 1] = x.y; v[4 * j + 2] = x.z; v[4 * j + 3] = x.w;
       }
     } else {
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(W) + i * 32);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint4 x = __ldg(src + j);
+        const uint4 x = __ldca(src + j);
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -79,8 +79,8 @@ pack_mxfp4_codes_kernel(const uint8_t* __restrict__ codes, const uint8_t* __rest
        i += (long long)gridDim.x * blockDim.x) {
     const long long row = i / bpr;
     const int b = (int)(i % bpr), n = (int)(row % N), r = n % kTileN;
-    const uint4 c = __ldg(reinterpret_cast<const uint4*>(codes) + i);
-    const uint8_t sc = __ldg(scales + i);
+    const uint4 c = __ldca(reinterpret_cast<const uint4*>(codes) + i);
+    const uint8_t sc = __ldca(scales + i);
     if (sc == 0xFFu) set_status(status, GSG_ERR_NONFINITE);   // UE8M0's NaN
     uint8_t* cb = mx_chunk(packed, row / N, n, b >> 3, NT, KC);
     *reinterpret_cast<uint4*>(cb + r * 128 + (b & 7) * 16) = c;
@@ -148,13 +148,13 @@ act_quant_mx_kernel(const MxQuantParams p) {
     uint32_t w[kVals / 2];
 #pragma unroll
     for (int i = 0; i < kVals / 8; ++i) {
-      const uint4 x = valid ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+      const uint4 x = valid ? __ldca(src + i) : make_uint4(0u, 0u, 0u, 0u);
       w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
     }
     int rows[kMxRowsAhead];
 #pragma unroll
     for (int j = 0; j < kMxRowsAhead; ++j)
-      rows[j] = (valid && j < p.k) ? (p.inv_perm != nullptr ? __ldg(p.inv_perm + (size_t)t * p.k + j) : t) : -1;
+      rows[j] = (valid && j < p.k) ? (p.inv_perm != nullptr ? __ldca(p.inv_perm + (size_t)t * p.k + j) : t) : -1;
     uint32_t m2 = 0;   // maxima of the even and the odd values' magnitudes, as bf16 bits
 #pragma unroll
     for (int i = 0; i < kVals / 2; ++i) m2 = __vmaxu2(m2, w[i] & 0x7FFF7FFFu);
@@ -204,7 +204,7 @@ act_quant_mx_kernel(const MxQuantParams p) {
 #pragma unroll
     for (int j = 0; j < kMxRowsAhead; ++j)
       if (j < p.k) dispatch(rows[j]);
-    for (int j = kMxRowsAhead; j < p.k; ++j) dispatch(__ldg(p.inv_perm + (size_t)t * p.k + j));
+    for (int j = kMxRowsAhead; j < p.k; ++j) dispatch(__ldca(p.inv_perm + (size_t)t * p.k + j));
   }
 }
 

@@ -12,7 +12,7 @@
 // (see round_odd), so that its later rounding to a code or to bf16 is the rounding of the value before it,
 // not of a value that has been rounded onto a border between two codes: with sums of eight squares in fp32,
 // which is 2^-31 off, a few of 58.7 million codes still came out on the wrong side.  (h may be the
-// residual's own buffer: each thread reads its values, through the coherent path, before it stores them.)
+// residual's own buffer: each thread reads its values before it stores them.)
 #include "gsg_launch.h"
 #include "gsg_mx.cuh"
 
@@ -31,6 +31,18 @@ struct NormParams {
   int w_f32;
   int* status;
 };
+
+// 16 bytes where `on`, else zeros.  (An ordinary load, see pdl_wait; from L2, since a row is read once.)
+__device__ __forceinline__ uint4 load_l2(bool on, const void* p) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@q ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((uint32_t)on));
+  return v;
+}
 
 __device__ __forceinline__ double warp_sum_d(double v) {
 #pragma unroll
@@ -80,7 +92,7 @@ constexpr int kNormThreads = 512;
 template <int kRes, int kBits, int kU>
 __global__ void __launch_bounds__(kNormThreads, kU == 2 && kBits != 0 ? 3 : 0)
 add_rmsnorm_kernel(const NormParams p) {
-  __shared__ double red[32], inv_rms;
+  __shared__ double red[32];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -91,15 +103,14 @@ add_rmsnorm_kernel(const NormParams p) {
 #pragma unroll
   for (int i = 0; i < kU; ++i) {
     const int u = i * blockDim.x + threadIdx.x;
-    xq[i] = u < upr ? __ldg(reinterpret_cast<const uint4*>(p.x + row) + u) : make_uint4(0u, 0u, 0u, 0u);
+    xq[i] = load_l2(u < upr, p.x + row + 8 * (size_t)u);
   }
   if (kRes == 1) {
     uint4 rq[kU];
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       const int u = i * blockDim.x + threadIdx.x;
-      rq[i] = u < upr ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.r) + row)[u]
-                      : make_uint4(0u, 0u, 0u, 0u);
+      rq[i] = load_l2(u < upr, static_cast<const uint16_t*>(p.r) + row + 8 * (size_t)u);
     }
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
@@ -115,21 +126,22 @@ add_rmsnorm_kernel(const NormParams p) {
       unpack8_bf16(hq, v[i]);
     }
   } else if (kRes == 2) {
-    float4 rq[kU][2];
+    uint4 rq[kU][2];
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       const int u = i * blockDim.x + threadIdx.x;
-      const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.r) + row) + 2 * u;
-      rq[i][0] = u < upr ? src[0] : make_float4(0.f, 0.f, 0.f, 0.f);
-      rq[i][1] = u < upr ? src[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float* src = static_cast<const float*>(p.r) + row + 8 * (size_t)u;
+      rq[i][0] = load_l2(u < upr, src);
+      rq[i][1] = load_l2(u < upr, src + 4);
     }
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       const int u = i * blockDim.x + threadIdx.x;
       unpack8_bf16(xq[i], v[i]);
-      const float b[8] = {rq[i][0].x, rq[i][0].y, rq[i][0].z, rq[i][0].w, rq[i][1].x, rq[i][1].y, rq[i][1].z, rq[i][1].w};
+      const uint32_t rb[8] = {rq[i][0].x, rq[i][0].y, rq[i][0].z, rq[i][0].w,
+                              rq[i][1].x, rq[i][1].y, rq[i][1].z, rq[i][1].w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = __fadd_rn(v[i][j], b[j]);
+      for (int j = 0; j < 8; ++j) v[i][j] = __fadd_rn(v[i][j], __uint_as_float(rb[j]));
       if (u < upr) {
         float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.h) + row) + 2 * u;
         dst[0] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
@@ -155,14 +167,8 @@ add_rmsnorm_kernel(const NormParams p) {
     if (!(var < (double)INFINITY) && threadIdx.x == 0) set_status(p.status, GSG_ERR_NONFINITE);
     return;
   }
-  // (the units below find such a row too; with two of them the branch keeps the compiler within the registers)
-  if (kU == 2 && !(var > 0.0 && var < (double)INFINITY) && threadIdx.x == 0) set_status(p.status, GSG_ERR_NONFINITE);
   const double rd = rsqrt(var);
   const float rh = (float)rd, rl = (float)(rd - (double)rh);
-  if (kU == 2) {   // (with two units a thread it costs the registers of a third block)
-    if (lane == 0) inv_rms = rd;   // (every warp writes the same)
-    __syncwarp();
-  }
   // |h| rh is at most sqrt(K), whatever the weights: a product with w past the range is a y past the range.  What is
   // carried along underflows for y below 2^-100 or h below 2^-100 of the row's rms only.
   const bool middle = rh > 0x1p-60f && rh < 0x1p60f;
@@ -189,17 +195,21 @@ add_rmsnorm_kernel(const NormParams p) {
       y[j] = round_odd(s, __fadd_rn(__fmaf_rn(q, w[j], -s), c));
     }
     if (!middle) {
-      const double r = kU == 2 ? *const_cast<volatile double*>(&inv_rms) : rd;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         float h = v[i][j];
+        // (the weight from memory again: the eight of a unit held until here would be registers that every row misses)
+        const float wj = !in       ? 0.0f
+                         : p.w_f32 ? static_cast<const volatile float*>(p.w)[8 * u + j]
+                                   : bf16_bits_to_f32(static_cast<const volatile uint16_t*>(p.w)[8 * u + j]);
         asm volatile("" : "+f"(h));   // not the sum's conversion kept in a register pair until here
-        const double d = (double)h * (double)w[j] * r;
+        const double d = (double)h * (double)wj * rd;
         const float s = (float)d;
         y[j] = round_odd(s, (float)(d - (double)s));
       }
     }
-    // a y that is not finite, as every one is of a row without a norm (v 0, infinite or NaN), or that bf16 does not hold
+    // a y that is not finite, as every one is of a row without a norm (v 0, infinite or NaN), or that bf16 does not
+    // hold
     float top = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(y[j]));

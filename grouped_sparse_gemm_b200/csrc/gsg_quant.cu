@@ -56,10 +56,10 @@ struct QuantParams {
 // every thread of the block must call it).
 __device__ __forceinline__ float quant_tensor_scale(const QuantParams& p, float* red, float* s_sh) {
   if (p.s_in != nullptr) {
-    if (threadIdx.x == 0) *s_sh = __ldg(p.s_in);
+    if (threadIdx.x == 0) *s_sh = __ldca(p.s_in);
   } else {
     float v = 0.0f;
-    for (int i = threadIdx.x; i < p.nparts; i += blockDim.x) v = fmaxf(v, p.partial[i]);
+    for (int i = threadIdx.x; i < p.nparts; i += blockDim.x) v = fmaxf(v, __ldca(p.partial + i));
     v = warp_max(v);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
@@ -112,10 +112,10 @@ __device__ __forceinline__ void quant32_fetch(const QuantParams& p, long long u,
   q.b = int(u32 % (unsigned)bpr);
   const uint4* src = reinterpret_cast<const uint4*>(p.X + (size_t)q.t * p.K + (size_t)q.b * 32);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q.x[i] = q.valid ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+  for (int i = 0; i < 4; ++i) q.x[i] = q.valid ? __ldca(src + i) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
   for (int j = 0; j < kQ32Rows; ++j)
-    q.rows[j] = (q.valid && j < p.k) ? (p.inv_perm != nullptr ? __ldg(p.inv_perm + (size_t)q.t * p.k + j) : q.t) : -1;
+    q.rows[j] = (q.valid && j < p.k) ? (p.inv_perm != nullptr ? __ldca(p.inv_perm + (size_t)q.t * p.k + j) : q.t) : -1;
 }
 
 __global__ void __launch_bounds__(128)
@@ -180,7 +180,7 @@ act_quant32_kernel(QuantParams p) {
 #pragma unroll
     for (int j = 0; j < kQ32Rows; ++j)
       if (j < p.k) dispatch(q.rows[j]);
-    for (int j = kQ32Rows; j < p.k; ++j) dispatch(__ldg(p.inv_perm + (size_t)q.t * p.k + j));
+    for (int j = kQ32Rows; j < p.k; ++j) dispatch(__ldca(p.inv_perm + (size_t)q.t * p.k + j));
   }
   if (p.raw == nullptr) quant_zero_padding(p);
 }
@@ -202,7 +202,7 @@ act_scales_quad_kernel(const uint32_t* __restrict__ raw, int R, int KBa, int rca
   for (int i = threadIdx.x; i < (kQuadTileRows + 96) * kQuadTileKb; i += blockDim.x) {
     const int rr = i / kQuadTileKb, kk = i % kQuadTileKb;
     const int row = r0 + rr, kb = kb0 + kk;
-    tile[rr][kk] = (row < R && kb < KBa) ? __ldg(raw + (size_t)row * KBa + kb) : 0u;
+    tile[rr][kk] = (row < R && kb < KBa) ? __ldca(raw + (size_t)row * KBa + kb) : 0u;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < kQuadTileRows * kQuadTileKb; i += blockDim.x) {
@@ -226,8 +226,8 @@ __device__ __forceinline__ void quant_fetch(const QuantParams& p, long long base
   const unsigned b32 = (unsigned)base;   // U = T*K/8 < 2^31 is checked on the host
   const int t = int(b32 / (unsigned)units_per_row);
   const int c8 = int(b32 % (unsigned)units_per_row) + lane;
-  q.x = __ldg(reinterpret_cast<const uint4*>(p.X + (size_t)t * p.K + (size_t)c8 * 8));
-  q.myrow = lane < p.k ? (p.inv_perm != nullptr ? __ldg(p.inv_perm + (size_t)t * p.k + lane) : t) : -1;
+  q.x = __ldca(reinterpret_cast<const uint4*>(p.X + (size_t)t * p.K + (size_t)c8 * 8));
+  q.myrow = lane < p.k ? (p.inv_perm != nullptr ? __ldca(p.inv_perm + (size_t)t * p.k + lane) : t) : -1;
 }
 
 __global__ void __launch_bounds__(kQuantMainThreads)
@@ -289,7 +289,7 @@ act_quant_kernel(QuantParams p) {
     int myrow = q.myrow;
     for (int j0 = 0; j0 < p.k; j0 += 32) {
       if (j0 > 0)
-        myrow = j0 + lane < p.k ? (p.inv_perm != nullptr ? __ldg(p.inv_perm + (size_t)t * p.k + j0 + lane) : t) : -1;
+        myrow = j0 + lane < p.k ? (p.inv_perm != nullptr ? __ldca(p.inv_perm + (size_t)t * p.k + j0 + lane) : t) : -1;
       const int jn = min(32, p.k - j0);
       for (int j = 0; j < jn; ++j) {
         const int row = __shfl_sync(0xffffffffu, myrow, j);

@@ -56,7 +56,7 @@ __device__ __forceinline__ void warp_load_ids(const int32_t* __restrict__ ids, i
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int f = f0 + 32 * i + lane;
-    x[i] = f < f1 ? __ldg(ids + f) : -1;
+    x[i] = f < f1 ? __ldca(ids + f) : -1;
   }
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -245,13 +245,13 @@ route_scan_kernel(const int* ws_hist, int nchunks, int E, int32_t* off, int* ws_
   const int e = threadIdx.x;
   int tot = 0;
   if (e < E)
-    for (int b = 0; b < nchunks; ++b) tot += ws_hist[(size_t)b * E + e];
+    for (int b = 0; b < nchunks; ++b) tot += __ldca(ws_hist + (size_t)b * E + e);
   const int start = block_exclusive_scan(tot, warp_sums, &total);
   if (e < E) {
     off[e] = start;
     int run = start;
     for (int b = 0; b < nchunks; ++b) {
-      int c = ws_hist[(size_t)b * E + e];
+      int c = __ldca(ws_hist + (size_t)b * E + e);
       ws_base[(size_t)b * E + e] = run;
       run += c;
     }
@@ -278,7 +278,7 @@ route_scatter_kernel(const int32_t* __restrict__ ids, int R, int E, const int* w
     int tot = 0, before = 0;
     if (e < E)
       for (int b = 0; b < nchunks; ++b) {
-        const int c = ws[(size_t)b * E + e];
+        const int c = __ldca(ws + (size_t)b * E + e);
         tot += c;
         if (b < (int)blockIdx.x) before += c;
       }
@@ -301,7 +301,7 @@ route_scatter_kernel(const int32_t* __restrict__ ids, int R, int E, const int* w
   warp_histogram<kPer>(x, m, f0, f1, hist + warp * E, key_bits(E));
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    int run = kSelfScan ? chunk_base : ws[(size_t)blockIdx.x * E + e];
+    int run = kSelfScan ? chunk_base : __ldca(ws + (size_t)blockIdx.x * E + e);
     for (int w = 0; w < 32; ++w) {
       int c = hist[w * E + e];
       hist[w * E + e] = run;

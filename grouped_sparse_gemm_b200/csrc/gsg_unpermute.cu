@@ -34,12 +34,12 @@ unpermute_kernel(const uint16_t* __restrict__ Y, const int32_t* __restrict__ inv
 #pragma unroll
       for (int jj = 0; jj < 8; ++jj) {
         const bool in = j0 + jj < k;
-        row[jj] = in ? __ldg(inv_perm + (size_t)t * k + j0 + jj) : -1;
-        g[jj] = in ? __ldg(gates + (size_t)t * k + j0 + jj) : 0.0f;
+        row[jj] = in ? __ldca(inv_perm + (size_t)t * k + j0 + jj) : -1;
+        g[jj] = in ? __ldca(gates + (size_t)t * k + j0 + jj) : 0.0f;
       }
 #pragma unroll
       for (int jj = 0; jj < 8; ++jj)
-        v[jj] = (row[jj] >= 0 && row[jj] < R) ? __ldg(reinterpret_cast<const uint4*>(Y + (size_t)row[jj] * N) + c)
+        v[jj] = (row[jj] >= 0 && row[jj] < R) ? __ldca(reinterpret_cast<const uint4*>(Y + (size_t)row[jj] * N) + c)
                                               : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int jj = 0; jj < 8; ++jj) {
