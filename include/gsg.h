@@ -299,8 +299,10 @@ gsg_status_t gsg_grouped_sparse_gemm_combine(const uint8_t* a_codes, const uint8
  * ((e*NT + nt)*(K/256) + kc) * 17408:
  *   codes  r*128 + c for row r (0..127) of the n-tile and byte c of the chunk's 256 codes of that row.
  *   scales 16384 + h*512 + 16*(r%32) + 4*(r/32) + j for 32-block 4*h + j of the chunk.
- * 4.25 bit/weight.  w_packed must be 128-byte aligned.  E <= 1024 and E*N*K*17/4096 < 2^31 (rows of 128
- * bytes), else GSG_ERR_UNSUPPORTED_SHAPE.
+ * 4.25 bit/weight.  w_packed must be 128-byte aligned.  N % 128 == 0, K % 256 == 0, E <= 1024 and
+ * E*N*K*17/4096 < 2^31 (rows of 128 bytes), else GSG_ERR_UNSUPPORTED_SHAPE.  Other shapes are padded by the
+ * caller: codes 0 under any scale but 0xFF add nothing, so K grows by zero codes of the weights and zero columns of
+ * X, N by zero rows, whose columns of Y are dropped.
  * Activations: codes [R][K/2] (MXFP4) or [R][K] (MXFP8); scales [K/128][R][4][4 B], entry (kb, r, c, j) =
  * scale byte of block 4*kb + j of row r + 32*c (0 when r + 32*c >= R): the quad layout above without its
  * padding rows.
@@ -348,8 +350,10 @@ gsg_status_t gsg_add_rmsnorm_mx(const uint16_t* x, const void* residual, int res
  *     Y[r][n] = sum_k a[r][k] * w[e][n][k]      (fp32 accumulation)
  * a_codes / a_scales in act_fmt from gsg_quantize_act_mx or gsg_add_rmsnorm_mx, w_packed from
  * gsg_pack_mxfp4 or gsg_pack_mxfp4_codes.  Everything else (offsets, the max_rows_per_expert hint, Y, rows
- * that are not written) as for gsg_grouped_sparse_gemm.  E = 1 with offsets {0, R} is a plain linear layer.
- * No workspace. */
+ * that are not written) as for gsg_grouped_sparse_gemm.  The hint may be -1 where the host does not know the
+ * routing: tiles of 16 and 32 tokens are chosen with it only, which takes 0 to 5 % off decode on 128 experts and
+ * adds 8 to 13 % on 384 (K 768, N 2048, 64 and 256 tokens top-8).  E = 1 with offsets {0, R} is a plain linear
+ * layer.  No workspace. */
 gsg_status_t gsg_grouped_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int act_fmt,
                                  const uint8_t* w_packed, const int32_t* expert_offsets, int E, int N, int K, int R,
                                  int max_rows_per_expert, void* Y, int y_dtype, void* stream);

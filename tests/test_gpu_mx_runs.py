@@ -60,3 +60,20 @@ def test_runs_are_bit_identical(gsg, fmt, N, mean):
         gsg.grouped_mx_gemm(a, w, off, out=y)
         differ += (y.view(torch.int16) != want.view(torch.int16)).any()
     assert int(differ) == 0
+
+
+@pytest.mark.parametrize("fmt", [4, 8])
+def test_other_shapes_padded_with_zeros(gsg, fmt):
+    """Widths that are no multiple of 256 and 128: zero codes, zero columns of X, dropped columns of Y."""
+    E, N, K, Np, Kp = 3, 200, 352, 256, 512
+    codes, sc = weights(E, N, K, 8)
+    off, x = layout([40, 0, 77], K, 9)
+    pc, ps, px = np.zeros((E, Np, Kp), np.uint8), np.zeros((E, Np, Kp // 32), np.uint8), torch.zeros(117, Kp, dtype=x.dtype)
+    pc[:, :N, :K], ps[:, :N, :K // 32], px[:, :K] = codes, sc, x
+    ps[:, N:], ps[:, :, K // 32:] = 254, 200     # (any scale)
+    a = gsg.quantize_act_mx(px.to(DEV), fmt)
+    y = gsg.grouped_mx_gemm(a, pack(gsg, pc, ps), torch.from_numpy(off).to(DEV), out_dtype=torch.float32)[:, :N]
+    A = omx.dequantize(*omx.quantize(x.double().numpy(), fmt), fmt)
+    for e in (0, 2):
+        yr, b = ogemm.gemm_rows(A[off[e]:off[e + 1]], omx.dequantize(codes[e], sc[e], 4), 1.0)
+        tl.assert_gemm_close(y[off[e]:off[e + 1]], yr, b, f"expert {e}")
