@@ -163,14 +163,25 @@ def _on_stream(fn, stream, *args):
     """fn(*args), a call of this module, with `stream` current.  What it allocates is that stream's memory: neither
     what the stream current until now has yet to write, nor given to it while the call still runs.  That stream
     may read the outputs (once it waits for `stream`), also if they are dropped before it has."""
-    now = torch.cuda.current_stream()
-    if stream.cuda_stream == now.cuda_stream:
+    # (by the stream's numbers: torch.cuda.stream() and the Stream objects that it makes take 15 us)
+    now = torch._C._cuda_getCurrentStream(torch.cuda.current_device())
+    new = (stream.stream_id, stream.device_index, stream.device_type)
+    if new == now:
         return fn(*args)
-    with torch.cuda.stream(stream):
+    _set_stream(new)
+    try:
         out = fn(*args)
-    for t in _tensors(out):
-        t.record_stream(now)
+    finally:
+        _set_stream(now)
+    for o in out if isinstance(out, tuple) else (out,):
+        if not any(o is a for a in args):   # (not the caller's own buffers)
+            for t in _tensors(o):
+                t.record_stream(torch.cuda.current_stream())
     return out
+
+
+def _set_stream(s) -> None:
+    torch._C._cuda_setStream(stream_id=s[0], device_index=s[1], device_type=s[2])
 
 
 def _need_cuda(*ts: Optional[torch.Tensor]):
