@@ -4,9 +4,9 @@
 //   y = h * w / sqrt(v);   outputs: h, y in bf16, y in MXFP8 or MXFP4 (from the unrounded y)
 //
 // A block holds one row in registers, so every input is read once and every output written once: bound by HBM, 8192
-// x 7168 with an fp32 residual, bf16 y and 8-bit codes 119 us = 6.4 TB/s; 512 x 2048 4.3 us, one row 3.5 us (latency).
-// Kept up for seconds it takes 134 us, at the board's power limit; squares summed in plain fp32 did not change that (134
-// us), and in fp32 with the rounding errors carried along it took 143 us.
+// x 7168 with an fp32 residual, bf16 y and 8-bit codes 119 us = 6.4 TB/s; 512 x 2048 5.1 us, one row 3.5 us (latency).
+// Kept up for seconds it takes 134 to 141 us, at the board's power limit; squares summed in plain fp32 did not change
+// that, and in fp32 with the rounding errors carried along they took 9 us more.
 // The squares are summed in 64 bits, and 1 / sqrt(v) is taken in 64 bits and applied as a sum of two fp32
 // numbers (in 64 bits throughout where those leave the fp32 range's middle).  y is rounded to fp32 "to odd"
 // (see round_odd), so that its later rounding to a code or to bf16 is the rounding of the value before it,
