@@ -102,7 +102,7 @@ template <typename T>
 __device__ __forceinline__ float lowest_logit() { return __uint_as_float(sizeof(T) == 4 ? 0xFF7FFFFFu : 0xFF7F0000u); }
 
 __device__ __forceinline__ float bias_of(const GateParams& p, int e) {
-  return p.bias != nullptr ? __ldg(p.bias + e) : 0.0f;
+  return p.bias != nullptr ? __ldca(p.bias + e) : 0.0f;
 }
 
 // Scores in 32 bits; softmax: mx the row's largest logit, inv_sum 1 / its denominator.  Two hardware

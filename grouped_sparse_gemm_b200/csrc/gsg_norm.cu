@@ -180,11 +180,11 @@ add_rmsnorm_kernel(const NormParams p) {
     float w[8];
     if (p.w_f32) {
       const float4* src = reinterpret_cast<const float4*>(p.w) + 2 * u;
-      const float4 a = in ? __ldg(src) : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float4 b = in ? __ldg(src + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 a = in ? __ldca(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 b = in ? __ldca(src + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
       w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
     } else {
-      unpack8_bf16(in ? __ldg(reinterpret_cast<const uint4*>(p.w) + u) : make_uint4(0u, 0u, 0u, 0u), w);
+      unpack8_bf16(in ? __ldca(reinterpret_cast<const uint4*>(p.w) + u) : make_uint4(0u, 0u, 0u, 0u), w);
     }
     float y[8];
 #pragma unroll

@@ -98,3 +98,36 @@ def test_layers_in_a_row_on_the_same_buffers(gsg, kind, sizes):
     torch.cuda.synchronize()
     assert int(differ) == 0
     del graph
+
+
+@pytest.mark.parametrize("T", [1, 16, 200])
+def test_weights_and_bias_changed_between_replays(gsg, T):
+    """The norm's weight and the router's bias are rewritten in place, by the framework's own copies, between
+    replays of a graph that reads them in every kernel."""
+    E, K, k = 64, 1024, 4
+    g = torch.Generator(device=DEV).manual_seed(8)
+    x = torch.randn(T, K, generator=g, device=DEV).to(BF)
+    logits = torch.randn(T, E, generator=g, device=DEV)
+    sets = [(1 + 0.1 * torch.randn(K, generator=g, device=DEV), 0.3 * torch.randn(E, generator=g, device=DEV))
+            for _ in range(3)]
+    want = [(gsg.add_rmsnorm_mx(x, w), gsg.moe_gate(logits, k, "sigmoid", bias=b)) for w, b in sets]
+    w, b = sets[0][0].clone(), sets[0][1].clone()
+    outs = []
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(6):
+            outs.append((gsg.add_rmsnorm_mx(x, w), gsg.moe_gate(logits, k, "sigmoid", bias=b)))
+    differ = torch.zeros((), dtype=torch.int64, device=DEV)
+    for i in range(300):
+        w.copy_(sets[i % 3][0])
+        b.copy_(sets[i % 3][1])
+        graph.replay()
+        n, (ids, gates) = want[i % 3]
+        for m, (jds, hates) in (outs[0], outs[-1]):
+            differ.add_((m.act.codes != n.act.codes).any())
+            differ.add_((m.y.view(torch.int16) != n.y.view(torch.int16)).any())
+            differ.add_((jds != ids).any())
+            differ.add_((hates != gates).any())
+    torch.cuda.synchronize()
+    assert int(differ) == 0
+    del graph
