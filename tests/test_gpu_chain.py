@@ -62,7 +62,27 @@ def nvfp4_layer(gsg, E, N, K, T, k, separate):
     return run, inputs
 
 
-LAYERS = [("mx", (64, 1024, 2048, 64, 8, 8)), ("mx", (8, 1024, 1024, 16, 2, 4)), ("mx", (8, 256, 512, 1, 2, 8)),
+def fused_layer(gsg, E, K, I, T, k):
+    """Routing and quantizer -> up-projection with SwiGLU -> down-projection with the combine."""
+    g = torch.Generator(device=DEV).manual_seed(9)
+    up = gsg.pack_sparse_nvfp4(torch.randn(E, 2 * I, K, generator=g, device=DEV) * 0.05)
+    down = gsg.pack_sparse_nvfp4(torch.randn(E, K, I, generator=g, device=DEV) * 0.05)
+    h_scale = torch.full((1,), 0.002, device=DEV)
+    comb = gsg.combine_workspace(E, K, I, T, k, DEV)
+    inputs = [(torch.randn(T, K, generator=g, device=DEV).to(BF),
+               torch.rand(T, E, generator=g, device=DEV).topk(k, dim=1)[1].to(torch.int32),
+               torch.rand(T, k, generator=g, device=DEV)) for _ in range(2)]
+
+    def run(x, o):
+        r, a = gsg.moe_dispatch_nvfp4(x[1], x[0], E, out_route=o.get("r"), out_act=o.get("a"), workspace=o.get("ws"))
+        h = gsg.grouped_sparse_gemm_swiglu(a, up, r.offsets, h_scale, out=o.get("h"))
+        out = gsg.grouped_sparse_gemm_combine(h, down, r, x[2], comb, out=o.get("out"))
+        return dict(r=r, a=a, h=h, out=out, ws=torch.empty(1 << 20, dtype=torch.uint8, device=DEV))
+    return run, inputs
+
+
+LAYERS = [("fused", (8, 512, 256, 16, 2)), ("fused", (64, 1024, 512, 64, 8)), ("fused", (16, 1024, 512, 700, 4)),
+          ("mx", (64, 1024, 2048, 64, 8, 8)), ("mx", (8, 1024, 1024, 16, 2, 4)), ("mx", (8, 256, 512, 1, 2, 8)),
           ("mx", (1, 1024, 2048, 300, 1, 8)), ("mx", (128, 768, 1024, 512, 8, 4)),
           ("nvfp4", (64, 1024, 2048, 64, 8, False)), ("nvfp4", (8, 1024, 1024, 16, 2, False)),
           ("nvfp4", (8, 1024, 1024, 16, 2, True)), ("nvfp4", (128, 768, 1024, 512, 8, True))]
@@ -70,7 +90,7 @@ LAYERS = [("mx", (64, 1024, 2048, 64, 8, 8)), ("mx", (8, 1024, 1024, 16, 2, 4)),
 
 @pytest.mark.parametrize("kind,sizes", LAYERS)
 def test_layers_in_a_row_on_the_same_buffers(gsg, kind, sizes):
-    run, inputs = (mx_layer if kind == "mx" else nvfp4_layer)(gsg, *sizes)
+    run, inputs = {"mx": mx_layer, "nvfp4": nvfp4_layer, "fused": fused_layer}[kind](gsg, *sizes)
     want = [run(x, {})["out"].clone() for x in inputs]      # each on buffers of its own
     o = run(inputs[0], {})
     torch.cuda.synchronize()
